@@ -16,12 +16,15 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import Any, NamedTuple
 
 ORDER_DROP, ORDER_ZERO, ORDER_FIRST, ORDER_HYBRID = -1, 0, 1, 2
 
 __all__ = [
     "ORDER_DROP", "ORDER_ZERO", "ORDER_FIRST", "ORDER_HYBRID", "PisaError", "Shape", "HostOptions", "lib", "block_stats", "select", "attention", "attention_simt",
     "pisa", "pisa_host", "pisa_host_static", "STATIC_WORKSPACE_BYTES", "host_workspace_bytes", "head_chunks", "device_error", "num_blocks", "LIB_PATH", "SYMBOLS", "routing_norms",
+    "window_attention", "window_attention_backward", "window_attention_backward_workspace", "PagedCache", "paged_cache",
+    "cache_write", "cache_read", "paged_attention", "paged_attention_workspace",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpisa.so")
@@ -31,6 +34,8 @@ SYMBOLS = (
     "pisa_block_stats", "pisa_select", "pisa_routing_norms", "pisa_attention", "pisa_attention_simt",
     "pisa_device_error", "pisa_status_string", "pisa_last_error", "pisa_version",
     "pisa_run_host_workspace", "pisa_run_host", "pisa_select_grouped", "pisa_run_host_static",
+    "pisa_window_attention", "pisa_window_attention_backward_workspace", "pisa_window_attention_backward",
+    "pisa_cache_write", "pisa_cache_read", "pisa_paged_attention_workspace", "pisa_paged_attention",
 )
 
 # PISA_STATIC_WORKSPACE_BYTES in include/pisa.h: the device region pisa_run_host_static uses
@@ -57,6 +62,28 @@ class HostOptions(ctypes.Structure):
                 ("candidates", ctypes.c_int32), ("chunks", ctypes.c_int32)]
 
 
+class WindowShape(ctypes.Structure):
+    """pisa_window_shape_t."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hq", "Hkv", "N", "d")]
+
+
+class Window(ctypes.Structure):
+    """pisa_window_t: reach to either side (-1: no limit) and first tokens that stay visible."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("left", "right", "sinks")]
+
+
+class CacheArgs(ctypes.Structure):
+    """pisa_cache_t."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("K", "V", "k_scale", "v_scale")] +
+                [(n, ctypes.c_int32) for n in ("num_pages", "Hkv", "page", "d", "type")])
+
+
+class Sequences(ctypes.Structure):
+    """pisa_sequences_t."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("page_table", "kv_lens", "q_lens")] +
+                [(n, ctypes.c_int32) for n in ("B", "N", "max_pages")])
+
+
 _lib = None
 
 
@@ -81,6 +108,14 @@ def lib():
     L.pisa_run_host_workspace.argtypes = [Shape, i32, i32, opts, ctypes.POINTER(ctypes.c_size_t)]
     L.pisa_run_host.argtypes = [vp, vp, vp, Shape, i32, i32, f32, opts, vp, ctypes.c_size_t, vp, vp]
     L.pisa_run_host_static.argtypes = [vp, vp, vp, Shape, i32, i32, f32, opts, vp, vp]
+    size_p = ctypes.POINTER(ctypes.c_size_t)
+    L.pisa_window_attention.argtypes = [vp, vp, vp, WindowShape, Window, f32, vp, vp, vp]
+    L.pisa_window_attention_backward_workspace.argtypes = [WindowShape, Window, size_p]
+    L.pisa_window_attention_backward.argtypes = [vp] * 6 + [WindowShape, Window, f32, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    L.pisa_cache_write.argtypes = [vp, vp, CacheArgs, Sequences, vp]
+    L.pisa_cache_read.argtypes = [CacheArgs, Sequences, vp, vp, vp]
+    L.pisa_paged_attention_workspace.argtypes = [CacheArgs, Sequences, i32, Window, size_p]
+    L.pisa_paged_attention.argtypes = [vp, CacheArgs, Sequences, i32, Window, f32, vp, vp, vp, ctypes.c_size_t, vp]
     L.pisa_device_error.argtypes = [vp]
     L.pisa_status_string.argtypes = [ctypes.c_int]
     L.pisa_status_string.restype = ctypes.c_char_p
@@ -89,7 +124,9 @@ def lib():
     L.pisa_version.argtypes = []
     for name in ("pisa_block_stats", "pisa_select", "pisa_routing_norms", "pisa_attention", "pisa_attention_simt",
                  "pisa_device_error", "pisa_version", "pisa_run_host_workspace", "pisa_run_host",
-                 "pisa_select_grouped", "pisa_run_host_static"):
+                 "pisa_select_grouped", "pisa_run_host_static", "pisa_window_attention",
+                 "pisa_window_attention_backward_workspace", "pisa_window_attention_backward", "pisa_cache_write",
+                 "pisa_cache_read", "pisa_paged_attention_workspace", "pisa_paged_attention"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -410,6 +447,244 @@ def pisa_host_static(Q, K, V, block: int, topk: int, order: int = 1, scale: floa
         _check(lib().pisa_run_host_static(_ptr(Q), _ptr(K), _ptr(V), s, int(topk), int(order), float(scale),
                                           ctypes.byref(o), _ptr(out), stream))
     return out
+
+
+def _heads(Q, K):
+    """(B, Hq, Hkv, N, d) of grouped-head operands [B, Hq, N, d] and [B, Hkv, N, d]."""
+    for t, name in ((Q, "Q"), (K, "K")):
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be a [B, H, N, d] tensor")
+    B, Hq, N, d = Q.shape
+    return B, Hq, K.shape[1], N, d
+
+
+def _window(left: int, right: int, sinks: int) -> Window:
+    for x, name in ((left, "left"), (right, "right"), (sinks, "sinks")):
+        if not -2 ** 31 <= int(x) < 2 ** 31:
+            raise ValueError(f"{name}={x} does not fit 32 bits")
+    return Window(int(left), int(right), int(sinks))
+
+
+def _require_all(checks, dev):
+    """``_require`` for (tensor, name, shape, dtype) entries; shapes and dtypes first, then the device."""
+    for t, name, shp, dt in checks:
+        _require(t, name, shp, dt)
+    for t, name, _, _ in checks:
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _workspace(t, nbytes: int, dev):
+    """The caller's workspace tensor (uint8, checked) or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    if t.numel() < nbytes:
+        raise ValueError(f"workspace holds {t.numel()} bytes, {nbytes} are needed")
+    if t.device != dev:
+        raise ValueError(f"workspace is on {t.device}, expected {dev}")
+    return t
+
+
+def window_attention(Q, K, V, left: int = -1, right: int = -1, sinks: int = 0, scale: float | None = None, out=None,
+                     lse=None):
+    """Self-attention in which the query at position p sees key j if ``j <= p + right`` and
+    (``j >= p - left`` or ``j < sinks``); -1 sets no limit on a side. Q: bf16 [B, Hq, N, d];
+    K, V: bf16 [B, Hkv, N, d], query head h reading key head ``h // (Hq // Hkv)``. Returns
+    (O bf16 [B, Hq, N, d], lse fp32 [B, Hq, N], the natural logarithm of each row's sum)."""
+    import torch
+    B, Hq, Hkv, N, d = _heads(Q, K)
+    checks = [(Q, "Q", (B, Hq, N, d), torch.bfloat16), (K, "K", (B, Hkv, N, d), torch.bfloat16),
+              (V, "V", (B, Hkv, N, d), torch.bfloat16)]
+    if out is not None:
+        checks.append((out, "O", (B, Hq, N, d), torch.bfloat16))
+    if lse is not None:
+        checks.append((lse, "lse", (B, Hq, N), torch.float32))
+    for t, name, shp, dt in checks:
+        _require(t, name, shp, dt)
+    dev = _device_of(Q)
+    _require_all(checks, dev)
+    scale = d ** -0.5 if scale is None else scale
+    O = torch.empty_like(Q) if out is None else out
+    lse = torch.empty((B, Hq, N), device=dev, dtype=torch.float32) if lse is None else lse
+    with torch.cuda.device(dev):
+        _check(lib().pisa_window_attention(_ptr(Q), _ptr(K), _ptr(V), WindowShape(B, Hq, Hkv, N, d),
+                                           _window(left, right, sinks), float(scale), _ptr(O), _ptr(lse), _stream(Q)))
+    return O, lse
+
+
+def window_attention_backward_workspace(B: int, Hq: int, Hkv: int, N: int, d: int, left: int = -1, right: int = -1,
+                                        sinks: int = 0) -> int:
+    """Device workspace (bytes) that ``window_attention_backward`` needs for this problem."""
+    n = ctypes.c_size_t(0)
+    _check(lib().pisa_window_attention_backward_workspace(WindowShape(B, Hq, Hkv, N, d), _window(left, right, sinks),
+                                                          ctypes.byref(n)))
+    return int(n.value)
+
+
+def window_attention_backward(dO, Q, K, V, O, lse, left: int = -1, right: int = -1, sinks: int = 0,
+                              scale: float | None = None, out=None, workspace=None):
+    """Gradients (dQ, dK, dV) of ``window_attention``'s O, from the gradient dO of O and the
+    forward call's operands and results (same window and scale). ``out`` = (dQ, dK, dV)
+    preallocated; ``workspace``: a uint8 tensor of at least
+    ``window_attention_backward_workspace`` bytes that no other call uses meanwhile."""
+    import torch
+    B, Hq, Hkv, N, d = _heads(Q, K)
+    q, kv = (B, Hq, N, d), (B, Hkv, N, d)
+    checks = [(dO, "dO", q, torch.bfloat16), (Q, "Q", q, torch.bfloat16), (K, "K", kv, torch.bfloat16),
+              (V, "V", kv, torch.bfloat16), (O, "O", q, torch.bfloat16), (lse, "lse", (B, Hq, N), torch.float32)]
+    if out is not None:
+        checks += [(t, name, s, torch.bfloat16) for t, name, s in zip(out, ("dQ", "dK", "dV"), (q, kv, kv))]
+    for t, name, shp, dt in checks:
+        _require(t, name, shp, dt)
+    dev = _device_of(Q)
+    _require_all(checks, dev)
+    scale = d ** -0.5 if scale is None else scale
+    nbytes = window_attention_backward_workspace(B, Hq, Hkv, N, d, left, right, sinks)
+    ws = _workspace(workspace, nbytes, dev)
+    dQ, dK, dV = (torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V)) if out is None else out
+    with torch.cuda.device(dev):
+        _check(lib().pisa_window_attention_backward(
+            _ptr(dO), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse), WindowShape(B, Hq, Hkv, N, d),
+            _window(left, right, sinks), float(scale), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(ws), ws.numel(), _stream(Q)))
+    return dQ, dK, dV
+
+
+class PagedCache(NamedTuple):
+    """A paged key/value cache (pisa_cache_t): K, V [num_pages, Hkv, page, d], bf16 or
+    float8_e4m3fn codes, the latter with fp32 scales [num_pages, Hkv, page]. Page size 16,
+    32, 64 or 128."""
+    K: Any
+    V: Any
+    k_scale: Any = None
+    v_scale: Any = None
+
+
+def paged_cache(num_pages: int, Hkv: int, page: int, d: int, dtype=None, device="cuda") -> PagedCache:
+    """An empty (zeroed) cache of ``dtype`` torch.bfloat16 (default) or torch.float8_e4m3fn."""
+    import torch
+    dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError(f"cache dtype {dtype} (must be bfloat16 or float8_e4m3fn)")
+    K, V = (torch.zeros((num_pages, Hkv, page, d), dtype=dtype, device=device) for _ in "KV")
+    if dtype == torch.bfloat16:
+        return PagedCache(K, V)
+    return PagedCache(K, V, *(torch.zeros((num_pages, Hkv, page), dtype=torch.float32, device=device) for _ in "KV"))
+
+
+def _cache_args(cache, page_table, kv_lens, q_lens, B: int, N: int, dev):
+    """(pisa_cache_t, pisa_sequences_t) of checked tensors on ``dev``."""
+    import torch
+    K = cache.K
+    if not isinstance(K, torch.Tensor) or K.dim() != 4:
+        raise ValueError("cache K must be a [num_pages, Hkv, page, d] tensor")
+    if K.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError(f"cache K has dtype {K.dtype}, expected bfloat16 or float8_e4m3fn")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 [B, max_pages] tensor")
+    max_pages = page_table.shape[1]
+    checks = [(K, "cache K", K.shape, K.dtype), (cache.V, "cache V", K.shape, K.dtype),
+              (page_table, "page_table", (B, max_pages), torch.int32), (kv_lens, "kv_lens", (B,), torch.int32)]
+    quantised = K.dtype != torch.bfloat16
+    if quantised:
+        checks += [(cache.k_scale, "k_scale", K.shape[:3], torch.float32),
+                   (cache.v_scale, "v_scale", K.shape[:3], torch.float32)]
+    if q_lens is not None:
+        checks.append((q_lens, "q_lens", (B,), torch.int32))
+    _require_all(checks, dev)
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    num_pages, Hkv, page, d = K.shape
+    scales = (at(cache.k_scale), at(cache.v_scale)) if quantised else (None, None)
+    return (CacheArgs(at(K), at(cache.V), *scales, num_pages, Hkv, page, d, int(quantised)),
+            Sequences(at(page_table), at(kv_lens), at(q_lens), B, N, max_pages))
+
+
+def cache_write(K, V, cache, page_table, kv_lens, q_lens=None):
+    """Append the new tokens' keys and values (bf16 [B, Hkv, N, d]) to the cache, quantised
+    as they are written if it holds 8 bits. Token t of sequence b goes to position
+    ``kv_lens[b] - q_lens[b] + t`` (``kv_lens`` counts the new tokens; ``q_lens`` defaults to
+    N each), in page ``page_table[b, position // page]``."""
+    import torch
+    if K.dim() != 4:
+        raise ValueError("K must be a [B, Hkv, N, d] tensor")
+    B, Hkv, N, d = K.shape
+    for t, name in ((K, "K"), (V, "V")):
+        _require(t, name, K.shape, torch.bfloat16)
+    dev = _device_of(K)
+    if V.device != dev:
+        raise ValueError(f"V is on {V.device}, expected {dev}")
+    c, s = _cache_args(cache, page_table, kv_lens, q_lens, B, N, dev)
+    if (c.Hkv, c.d) != (Hkv, d):
+        raise ValueError(f"the cache holds {c.Hkv} heads of {c.d}, K has {Hkv} of {d}")
+    with torch.cuda.device(dev):
+        _check(lib().pisa_cache_write(_ptr(K), _ptr(V), c, s, _stream(K)))
+
+
+def cache_read(cache, page_table, kv_lens, N: int, out=None):
+    """(K, V) bf16 [B, Hkv, N, d]: the first N tokens of every sequence. Rows behind a
+    sequence's last are left as they are in ``out`` = (K, V), zero without it."""
+    import torch
+    dev = _device_of(cache.K)
+    B = page_table.shape[0]
+    c, s = _cache_args(cache, page_table, kv_lens, None, B, N, dev)
+    shape = (B, c.Hkv, N, c.d)
+    if out is None:
+        out = tuple(torch.zeros(shape, dtype=torch.bfloat16, device=dev) for _ in "KV")
+    K, V = out
+    _require_all([(K, "K", shape, torch.bfloat16), (V, "V", shape, torch.bfloat16)], dev)
+    with torch.cuda.device(dev):
+        _check(lib().pisa_cache_read(c, s, _ptr(K), _ptr(V), _stream(K)))
+    return K, V
+
+
+def _paged_workspace(c, s, Hq: int, w) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().pisa_paged_attention_workspace(c, s, Hq, w, ctypes.byref(n)))
+    return int(n.value)
+
+
+def paged_attention_workspace(Q, cache, page_table, kv_lens, left: int = -1, right: int = 0, sinks: int = 0) -> int:
+    """Device workspace (bytes) that ``paged_attention`` needs for these operands."""
+    c, s = _cache_args(cache, page_table, kv_lens, None, Q.shape[0], Q.shape[2], Q.device)
+    return _paged_workspace(c, s, Q.shape[1], _window(left, right, sinks))
+
+
+def paged_attention(Q, cache, page_table, kv_lens, q_lens=None, left: int = -1, right: int = 0, sinks: int = 0,
+                    scale: float | None = None, out=None, lse=None, workspace=None):
+    """Attention of the new tokens Q (bf16 [B, Hq, N, d]; N = 1 for single tokens) over their
+    sequences in the cache, which holds the new tokens too. Positions, ``kv_lens`` and
+    ``q_lens`` as in ``cache_write``, the window as in ``window_attention`` (causal by
+    default). Returns (O bf16 [B, Hq, N, d], lse fp32 [B, Hq, N]); rows ``t >= q_lens[b]`` are
+    left as they are in ``out`` and ``lse``, zero without them. ``workspace``: a uint8 tensor
+    of at least ``paged_attention_workspace`` bytes that no other call uses meanwhile."""
+    import torch
+    if Q.dim() != 4:
+        raise ValueError("Q must be a [B, Hq, N, d] tensor")
+    B, Hq, N, d = Q.shape
+    checks = [(Q, "Q", (B, Hq, N, d), torch.bfloat16)]
+    if out is not None:
+        checks.append((out, "O", (B, Hq, N, d), torch.bfloat16))
+    if lse is not None:
+        checks.append((lse, "lse", (B, Hq, N), torch.float32))
+    for t, name, shp, dt in checks:
+        _require(t, name, shp, dt)
+    dev = _device_of(Q)
+    _require_all(checks, dev)
+    c, s = _cache_args(cache, page_table, kv_lens, q_lens, B, N, dev)
+    if c.d != d:
+        raise ValueError(f"the cache holds heads of {c.d}, Q has {d}")
+    w = _window(left, right, sinks)
+    scale = d ** -0.5 if scale is None else scale
+    ws = _workspace(workspace, _paged_workspace(c, s, Hq, w), dev)
+    new = torch.empty if q_lens is None else torch.zeros
+    O = new(Q.shape, dtype=Q.dtype, device=dev) if out is None else out
+    lse = new((B, Hq, N), dtype=torch.float32, device=dev) if lse is None else lse
+    with torch.cuda.device(dev):
+        _check(lib().pisa_paged_attention(_ptr(Q), c, s, Hq, w, float(scale), _ptr(O), _ptr(lse), _ptr(ws),
+                                          ws.numel(), _stream(Q)))
+    return O, lse
 
 
 def device_error(stream_tensor=None):

@@ -18,6 +18,8 @@
 #include "attention_tc.cuh"
 #include "stats_tc.cuh"
 #include "host_pipeline.cuh"
+#include "cache.cuh"
+#include "window_attention.cuh"
 
 using pisa::bf16;
 
@@ -810,7 +812,7 @@ pisa_status_t pisa_device_error(void* stream) {
       (e = cudaStreamSynchronize(st)) != cudaSuccess)
     return fail(PISA_ERR_CUDA, "device error word: %s", cudaGetErrorString(e));
   if (word & pisa::kErrTimeout) return fail(PISA_ERR_TIMEOUT, "a bounded device wait ran out (word=0x%x)", word);
-  if (word & pisa::kErrBadIndex) return fail(PISA_ERR_INVALID_ARG, "idx held an out-of-range block (word=0x%x)", word);
+  if (word & pisa::kErrBadIndex) return fail(PISA_ERR_INVALID_ARG, "idx held an out-of-range block, or a page or length was out of range (word=0x%x)", word);
   return ok();
 }
 
@@ -827,6 +829,8 @@ const char* pisa_status_string(pisa_status_t status) {
 
 const char* pisa_last_error(void) { return g_last_error.c_str(); }
 
-int32_t pisa_version(void) { return 200; }  // 0.2.0: orders -1 and 2, covariance-aware routing
+int32_t pisa_version(void) { return 300; }  // 0.3.0: windowed attention with gradients, paged cache
 
 }  // extern "C"
+
+#include "window_api.cuh"

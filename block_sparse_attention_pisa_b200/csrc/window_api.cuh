@@ -1,0 +1,290 @@
+// C ABI of the windowed attention, its gradient, the paged cache and the attention over it:
+// argument checks and launches. Included once by pisa_api.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+pisa_status_t check_aligned(const void* p, const char* name, unsigned align) {
+  if (p == nullptr) return fail(PISA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) & (align - 1u))
+    return fail(PISA_ERR_INVALID_ARG, "%s is not %u-byte aligned", name, align);
+  return ok();
+}
+
+pisa_status_t check_scale(float scale) {
+  if (!std::isfinite(scale) || !(scale > 0.f))
+    return fail(PISA_ERR_INVALID_ARG, "scale=%g (must be finite and > 0)", double(scale));
+  return ok();
+}
+
+// Heads, tokens and rows of any of these calls. Sets *empty if there is nothing to do.
+pisa_status_t check_heads(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int32_t d, bool* empty) {
+  *empty = false;
+  if (B < 0 || Hq < 0 || Hkv < 0 || N < 0)
+    return fail(PISA_ERR_INVALID_ARG, "negative shape (B=%lld Hq=%lld Hkv=%lld N=%lld)", (long long)B, (long long)Hq,
+                (long long)Hkv, (long long)N);
+  if (d <= 0) return fail(PISA_ERR_INVALID_ARG, "d must be positive (d=%d)", d);
+  if (B == 0 || Hq == 0 || N == 0) {
+    *empty = true;
+    return ok();
+  }
+  if (Hkv == 0 || Hq % Hkv != 0)
+    return fail(PISA_ERR_INVALID_ARG, "Hq=%lld is not a multiple of Hkv=%lld", (long long)Hq, (long long)Hkv);
+  if (d != 64 && d != 128) return fail(PISA_ERR_UNSUPPORTED, "head dimension d=%d (supported: 64, 128)", d);
+  if (N > pisa::kMaxTokens) return fail(PISA_ERR_UNSUPPORTED, "N=%lld exceeds %d", (long long)N, pisa::kMaxTokens);
+  // B * Hq * N < 2^31 without overflow: each factor is below 2^31
+  if (B * Hq > INT32_MAX || B * Hq * N > INT32_MAX)
+    return fail(PISA_ERR_UNSUPPORTED, "B*Hq*N exceeds 2^31 - 1 rows");
+  return ok();
+}
+
+pisa_status_t check_window(const pisa_window_t& w, pisa::Window* out) {
+  if (w.left < -1 || w.right < -1 || w.sinks < 0)
+    return fail(PISA_ERR_INVALID_ARG, "window left=%d right=%d (must be >= -1) sinks=%d (must be >= 0)", w.left,
+                w.right, w.sinks);
+  const auto reach = [](int32_t x) { return x < 0 || x > pisa::kMaxTokens ? pisa::kMaxTokens : x; };
+  *out = pisa::Window{reach(w.left), reach(w.right), reach(w.sinks)};
+  return ok();
+}
+
+pisa_status_t check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return ok();
+  PISA_TRY(check_aligned(ws, "workspace", 256));
+  if (have < need) return fail(PISA_ERR_INVALID_ARG, "workspace holds %zu bytes, %zu are needed", have, need);
+  return ok();
+}
+
+pisa_status_t check_cache(const pisa_cache_t& c, const pisa_sequences_t& s, int32_t Hq, bool* empty, pisa::Pages* g) {
+  PISA_TRY(check_heads(s.B, Hq, c.Hkv, s.N, c.d, empty));
+  if (*empty) return ok();
+  if (c.type != PISA_CACHE_BF16 && c.type != PISA_CACHE_E4M3)
+    return fail(PISA_ERR_INVALID_ARG, "cache type=%d (must be PISA_CACHE_BF16 or PISA_CACHE_E4M3)", c.type);
+  if (c.page <= 0 || c.num_pages <= 0 || s.max_pages <= 0)
+    return fail(PISA_ERR_INVALID_ARG, "page=%d num_pages=%d max_pages=%d (must be positive)", c.page, c.num_pages,
+                s.max_pages);
+  if (c.page != 16 && c.page != 32 && c.page != 64 && c.page != 128)
+    return fail(PISA_ERR_UNSUPPORTED, "page=%d (supported: 16, 32, 64, 128)", c.page);
+  if (int64_t(s.max_pages) * c.page > pisa::kMaxTokens)
+    return fail(PISA_ERR_UNSUPPORTED, "max_pages*page exceeds %d tokens", pisa::kMaxTokens);
+  if (int64_t(c.num_pages) * c.Hkv > INT32_MAX)
+    return fail(PISA_ERR_UNSUPPORTED, "num_pages*Hkv exceeds 2^31 - 1");
+  PISA_TRY(check_ptr(c.K, "cache K"));
+  PISA_TRY(check_ptr(c.V, "cache V"));
+  if (c.type == PISA_CACHE_E4M3) {
+    PISA_TRY(check_ptr(c.k_scale, "k_scale"));
+    PISA_TRY(check_ptr(c.v_scale, "v_scale"));
+  }
+  PISA_TRY(check_aligned(s.page_table, "page_table", 4));
+  PISA_TRY(check_aligned(s.kv_lens, "kv_lens", 4));
+  if (s.q_lens != nullptr) PISA_TRY(check_aligned(s.q_lens, "q_lens", 4));
+  int log_page = 4;
+  while ((1 << log_page) < c.page) ++log_page;
+  *g = pisa::Pages{c.K, c.V, c.k_scale, c.v_scale, s.page_table, s.kv_lens, s.q_lens, c.num_pages, s.max_pages, log_page};
+  return ok();
+}
+
+// the paged cache's kernels: a row per D/8 threads, kCacheRows rows in flight per thread
+template <typename Kernel>
+pisa_status_t launch_cache(Kernel k, const pisa::CacheParams& p, int d, int sms, cudaStream_t st, const char* what) {
+  const int64_t per = int64_t(pisa::kCacheThreads) / (d / 8);
+  const int64_t ctas = (p.rows + per - 1) / per;
+  const int64_t most = int64_t(sms) * 8;
+  k<<<unsigned(ctas < most ? ctas : most), pisa::kCacheThreads, 0, st>>>(p);
+  return check_launch(what);
+}
+
+template <int D, int KV>
+pisa_status_t launch_attend(const pisa::AttendParams& p, cudaStream_t st) {
+  const int64_t rows = int64_t(p.B) * p.Hq * p.N;
+  const unsigned grid = unsigned((rows + pisa::kRowWarps - 1) / pisa::kRowWarps);
+  pisa::attend_rows_kernel<D, KV><<<grid, 32 * pisa::kRowWarps, 0, st>>>(p);
+  return check_launch("attend_rows_kernel");
+}
+
+template <int D>
+pisa_status_t launch_attend_backward(const pisa::AttendParams& p, cudaStream_t st) {
+  const int64_t rows = int64_t(p.B) * p.Hq * p.N, keys = int64_t(p.B) * p.Hkv * p.N;
+  const unsigned gq = unsigned((rows + pisa::kRowWarps - 1) / pisa::kRowWarps);
+  const unsigned gk = unsigned((keys + pisa::kRowWarps - 1) / pisa::kRowWarps);
+  pisa::attend_delta_kernel<D><<<gq, 32 * pisa::kRowWarps, 0, st>>>(p);
+  PISA_TRY(check_launch("attend_delta_kernel"));
+  pisa::attend_dq_kernel<D><<<gq, 32 * pisa::kRowWarps, 0, st>>>(p);
+  PISA_TRY(check_launch("attend_dq_kernel"));
+  pisa::attend_dkv_kernel<D><<<gk, 32 * pisa::kRowWarps, 0, st>>>(p);
+  return check_launch("attend_dkv_kernel");
+}
+
+}  // namespace
+
+extern "C" {
+
+pisa_status_t pisa_window_attention(const void* Q, const void* K, const void* V, pisa_window_shape_t shape,
+                                    pisa_window_t window, float scale, void* O, float* lse, void* stream) {
+  bool empty = false;
+  PISA_TRY(check_heads(shape.B, shape.Hq, shape.Hkv, shape.N, shape.d, &empty));
+  pisa::AttendParams p{};
+  PISA_TRY(check_window(window, &p.win));
+  PISA_TRY(check_scale(scale));
+  if (empty) return ok();
+  PISA_TRY(check_ptr(Q, "Q"));
+  PISA_TRY(check_ptr(K, "K"));
+  PISA_TRY(check_ptr(V, "V"));
+  PISA_TRY(check_ptr(O, "O"));
+  if (lse != nullptr) PISA_TRY(check_aligned(lse, "lse", 4));
+  int sms = 0;
+  PISA_TRY(check_device(&sms));
+  p.Q = static_cast<const bf16*>(Q);
+  p.K = static_cast<const bf16*>(K);
+  p.V = static_cast<const bf16*>(V);
+  p.O = static_cast<bf16*>(O);
+  p.lse = lse;
+  p.B = shape.B;
+  p.Hq = shape.Hq;
+  p.Hkv = shape.Hkv;
+  p.N = shape.N;
+  p.scale = scale;
+  auto st = static_cast<cudaStream_t>(stream);
+  return shape.d == 128 ? launch_attend<128, pisa::kKvPlain>(p, st) : launch_attend<64, pisa::kKvPlain>(p, st);
+}
+
+pisa_status_t pisa_window_attention_backward_workspace(pisa_window_shape_t shape, pisa_window_t window,
+                                                       size_t* bytes) {
+  if (bytes == nullptr) return fail(PISA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = 0;
+  bool empty = false;
+  PISA_TRY(check_heads(shape.B, shape.Hq, shape.Hkv, shape.N, shape.d, &empty));
+  pisa::Window w;
+  PISA_TRY(check_window(window, &w));
+  if (empty) return ok();
+  *bytes = size_t(shape.B) * shape.Hq * shape.N * 4;  // delta
+  return ok();
+}
+
+pisa_status_t pisa_window_attention_backward(const void* dO, const void* Q, const void* K, const void* V,
+                                             const void* O, const float* lse, pisa_window_shape_t shape,
+                                             pisa_window_t window, float scale, void* dQ, void* dK, void* dV,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  PISA_TRY(pisa_window_attention_backward_workspace(shape, window, &need));
+  PISA_TRY(check_scale(scale));
+  if (need == 0) return ok();  // empty problem: nothing touched
+  pisa::AttendParams p{};
+  PISA_TRY(check_window(window, &p.win));
+  const void* bufs[8] = {dO, Q, K, V, O, dQ, dK, dV};
+  const char* names[8] = {"dO", "Q", "K", "V", "O", "dQ", "dK", "dV"};
+  for (int i = 0; i < 8; ++i) PISA_TRY(check_ptr(bufs[i], names[i]));
+  PISA_TRY(check_aligned(lse, "lse", 4));
+  PISA_TRY(check_workspace(workspace, workspace_bytes, need));
+  int sms = 0;
+  PISA_TRY(check_device(&sms));
+  p.Q = static_cast<const bf16*>(Q);
+  p.K = static_cast<const bf16*>(K);
+  p.V = static_cast<const bf16*>(V);
+  p.O = const_cast<bf16*>(static_cast<const bf16*>(O));
+  p.lse = const_cast<float*>(lse);
+  p.dO = static_cast<const bf16*>(dO);
+  p.dQ = static_cast<bf16*>(dQ);
+  p.dK = static_cast<bf16*>(dK);
+  p.dV = static_cast<bf16*>(dV);
+  p.delta = static_cast<float*>(workspace);
+  p.B = shape.B;
+  p.Hq = shape.Hq;
+  p.Hkv = shape.Hkv;
+  p.N = shape.N;
+  p.scale = scale;
+  auto st = static_cast<cudaStream_t>(stream);
+  return shape.d == 128 ? launch_attend_backward<128>(p, st) : launch_attend_backward<64>(p, st);
+}
+
+pisa_status_t pisa_cache_write(const void* K, const void* V, pisa_cache_t cache, pisa_sequences_t seqs,
+                               void* stream) {
+  bool empty = false;
+  pisa::CacheParams p{};
+  PISA_TRY(check_cache(cache, seqs, cache.Hkv, &empty, &p.pages));
+  if (empty) return ok();
+  PISA_TRY(check_ptr(K, "K"));
+  PISA_TRY(check_ptr(V, "V"));
+  int sms = 0;
+  PISA_TRY(check_device(&sms));
+  p.cK = cache.K;
+  p.cV = cache.V;
+  p.ks = cache.k_scale;
+  p.vs = cache.v_scale;
+  p.K = static_cast<const bf16*>(K);
+  p.V = static_cast<const bf16*>(V);
+  p.Hkv = cache.Hkv;
+  p.N = seqs.N;
+  p.rows = int64_t(seqs.B) * cache.Hkv * seqs.N;
+  auto st = static_cast<cudaStream_t>(stream);
+  const bool q = cache.type == PISA_CACHE_E4M3;
+  auto k = cache.d == 128 ? (q ? pisa::cache_write_kernel<128, true> : pisa::cache_write_kernel<128, false>)
+                          : (q ? pisa::cache_write_kernel<64, true> : pisa::cache_write_kernel<64, false>);
+  return launch_cache(k, p, cache.d, sms, st, "cache_write_kernel");
+}
+
+pisa_status_t pisa_cache_read(pisa_cache_t cache, pisa_sequences_t seqs, void* K, void* V, void* stream) {
+  bool empty = false;
+  pisa::CacheParams p{};
+  seqs.q_lens = nullptr;
+  PISA_TRY(check_cache(cache, seqs, cache.Hkv, &empty, &p.pages));
+  if (empty) return ok();
+  PISA_TRY(check_ptr(K, "K"));
+  PISA_TRY(check_ptr(V, "V"));
+  int sms = 0;
+  PISA_TRY(check_device(&sms));
+  p.oK = static_cast<bf16*>(K);
+  p.oV = static_cast<bf16*>(V);
+  p.Hkv = cache.Hkv;
+  p.N = seqs.N;
+  p.rows = int64_t(seqs.B) * cache.Hkv * seqs.N;
+  auto st = static_cast<cudaStream_t>(stream);
+  const bool q = cache.type == PISA_CACHE_E4M3;
+  auto k = cache.d == 128 ? (q ? pisa::cache_read_kernel<128, true> : pisa::cache_read_kernel<128, false>)
+                          : (q ? pisa::cache_read_kernel<64, true> : pisa::cache_read_kernel<64, false>);
+  return launch_cache(k, p, cache.d, sms, st, "cache_read_kernel");
+}
+
+pisa_status_t pisa_paged_attention_workspace(pisa_cache_t cache, pisa_sequences_t seqs, int32_t Hq,
+                                             pisa_window_t window, size_t* bytes) {
+  if (bytes == nullptr) return fail(PISA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = 0;
+  bool empty = false;
+  pisa::Pages g{};
+  PISA_TRY(check_cache(cache, seqs, Hq, &empty, &g));
+  pisa::Window w;
+  PISA_TRY(check_window(window, &w));
+  return ok();
+}
+
+pisa_status_t pisa_paged_attention(const void* Q, pisa_cache_t cache, pisa_sequences_t seqs, int32_t Hq,
+                                   pisa_window_t window, float scale, void* O, float* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  bool empty = false;
+  pisa::AttendParams p{};
+  PISA_TRY(check_cache(cache, seqs, Hq, &empty, &p.pages));
+  PISA_TRY(check_window(window, &p.win));
+  PISA_TRY(check_scale(scale));
+  if (empty) return ok();
+  PISA_TRY(check_ptr(Q, "Q"));
+  PISA_TRY(check_ptr(O, "O"));
+  if (lse != nullptr) PISA_TRY(check_aligned(lse, "lse", 4));
+  size_t need = 0;
+  PISA_TRY(pisa_paged_attention_workspace(cache, seqs, Hq, window, &need));
+  PISA_TRY(check_workspace(workspace, workspace_bytes, need));
+  int sms = 0;
+  PISA_TRY(check_device(&sms));
+  p.Q = static_cast<const bf16*>(Q);
+  p.O = static_cast<bf16*>(O);
+  p.lse = lse;
+  p.B = seqs.B;
+  p.Hq = Hq;
+  p.Hkv = cache.Hkv;
+  p.N = seqs.N;
+  p.scale = scale;
+  auto st = static_cast<cudaStream_t>(stream);
+  if (cache.type == PISA_CACHE_E4M3)
+    return cache.d == 128 ? launch_attend<128, pisa::kKvPagedE4m3>(p, st) : launch_attend<64, pisa::kKvPagedE4m3>(p, st);
+  return cache.d == 128 ? launch_attend<128, pisa::kKvPaged>(p, st) : launch_attend<64, pisa::kKvPaged>(p, st);
+}
+
+}  // extern "C"

@@ -262,11 +262,148 @@ pisa_status_t pisa_run_host_static(const void* Q, const void* K, const void* V, 
                                    int32_t order, float scale, const pisa_host_options_t* options, void* O,
                                    void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Windowed attention, its gradient, and attention over a paged cache
+ *
+ * Attention for sequences that see a token-exact window of themselves, and for sequences
+ * produced piece by piece: new tokens are appended to a cache and attend over it. Query
+ * heads may share key heads: query head h reads key head h / (Hq / Hkv).
+ *
+ * Window: a query at position p sees key j of its sequence if
+ *   j <= p + right  and  (j >= p - left  or  j < sinks).
+ * left and right count tokens; -1 sets no limit on that side (right = 0 is causal). The
+ * first `sinks` tokens stay visible to every later query. A row that sees no key has
+ * O = 0 and lse = -infinity.
+ *
+ *   s_j = scale q.k_j,  lse = log sum_j exp(s_j),  O = sum_j exp(s_j - lse) v_j
+ *
+ * Sums and softmax statistics are fp32; the weights exp(s_j - m) (m a running maximum) and
+ * the gradient's p_j and ds_j are rounded to bf16 for the tensor cores. A key or value that
+ * a row does not see but another row of the same 128-row tile does must be finite. Every
+ * sum runs in an order fixed by the shapes (and, over a cache, by the lengths): the same
+ * call gives the same bits.
+ * The conventions above hold (bf16, device pointers of the current device, contiguous,
+ * asynchronous, d in {64, 128}); pointers to int32 and to lse need 4-byte alignment only.
+ * No output may overlap an input.
+ * --------------------------------------------------------------------------------- */
+
+typedef struct {
+  int32_t B;    /* batch                                     */
+  int32_t Hq;   /* query heads, a multiple of Hkv            */
+  int32_t Hkv;  /* key/value heads                           */
+  int32_t N;    /* tokens of every sequence (true length)    */
+  int32_t d;    /* head dimension (64 or 128)                */
+} pisa_window_shape_t;
+
+typedef struct {
+  int32_t left;   /* tokens seen before the query's own (-1: all)  */
+  int32_t right;  /* tokens seen behind the query's own (-1: all)  */
+  int32_t sinks;  /* first tokens that stay visible                */
+} pisa_window_t;
+
+/*
+ * pisa_window_attention -- self-attention under the window.
+ * Q, O: bf16 [B, Hq, N, d]; K, V: bf16 [B, Hkv, N, d]; lse: fp32 [B, Hq, N] (natural
+ * logarithm) or NULL; scale finite and > 0.
+ */
+pisa_status_t pisa_window_attention(const void* Q, const void* K, const void* V, pisa_window_shape_t shape,
+                                    pisa_window_t window, float scale, void* O, float* lse, void* stream);
+
+/* Bytes of device workspace that pisa_window_attention_backward needs (no device is touched). */
+pisa_status_t pisa_window_attention_backward_workspace(pisa_window_shape_t shape, pisa_window_t window,
+                                                       size_t* bytes);
+
+/*
+ * pisa_window_attention_backward -- gradients of pisa_window_attention's O.
+ *   delta = dO.O,  p_j = exp(s_j - lse),  ds_j = p_j (dO.v_j - delta),
+ *   dQ = scale sum_j ds_j k_j,  dK_j = scale sum ds_j q,  dV_j = sum p_j dO
+ * (the sums of dK, dV over the rows that see j, of every query head of its group).
+ * O and lse as the forward call gave them; dO, dQ: bf16 [B, Hq, N, d]; dK, dV: bf16
+ * [B, Hkv, N, d], overwritten. workspace: device memory, 256-byte aligned, scratch; one
+ * call at a time may use it.
+ */
+pisa_status_t pisa_window_attention_backward(const void* dO, const void* Q, const void* K, const void* V,
+                                             const void* O, const float* lse, pisa_window_shape_t shape,
+                                             pisa_window_t window, float scale, void* dQ, void* dK, void* dV,
+                                             void* workspace, size_t workspace_bytes, void* stream);
+
+#define PISA_CACHE_BF16 0 /* rows as they are                                       */
+#define PISA_CACHE_E4M3 1 /* 8-bit floating point with an fp32 scale for every row  */
+
+/*
+ * A paged cache. Page i holds `page` consecutive tokens of one sequence for every key head:
+ * K, V: [num_pages, Hkv, page, d] (bf16, or e4m3 codes); k_scale, v_scale: fp32
+ * [num_pages, Hkv, page] (NULL for bf16). page in {16, 32, 64, 128}.
+ * A row (one token of one head) in 8 bits: scale = max(amax|x| / 448, 2^-126), codes =
+ * e4m3(x / scale), the value held is code * scale. A row with a NaN or an infinity is held
+ * as NaN, by its scale; the codes of every other row are finite, and a call that reads a
+ * cache expects that of codes it did not write itself.
+ */
+typedef struct {
+  void* K;
+  void* V;
+  float* k_scale;
+  float* v_scale;
+  int32_t num_pages;
+  int32_t Hkv;
+  int32_t page;
+  int32_t d;
+  int32_t type; /* PISA_CACHE_* */
+} pisa_cache_t;
+
+/*
+ * The sequences that a cache call works on. page_table: int32 [B, max_pages], the page that
+ * holds positions [i * page, (i + 1) * page) of a sequence (entries of pages that the call
+ * does not need may hold anything); kv_lens: int32 [B], tokens that the sequence holds, the
+ * new ones among them; q_lens: int32 [B], how many of the call's N tokens are real for each
+ * sequence, or NULL for all N. New token t of a sequence has position kv_len - q_len + t.
+ * The three are device data that the kernels check: a length outside [0, max_pages * page]
+ * (or [0, N]) is clamped, a needed entry outside [0, num_pages) is skipped (its tokens are
+ * not written, not read back and not seen), and either is flagged in the device error word.
+ */
+typedef struct {
+  const int32_t* page_table;
+  const int32_t* kv_lens;
+  const int32_t* q_lens;
+  int32_t B;
+  int32_t N;
+  int32_t max_pages;
+} pisa_sequences_t;
+
+/*
+ * pisa_cache_write -- appends the new tokens' keys and values to the cache.
+ * K, V: bf16 [B, Hkv, N, d]. Tokens t >= q_len and negative positions are not written. A
+ * page that a call writes belongs to one of its sequences only.
+ */
+pisa_status_t pisa_cache_write(const void* K, const void* V, pisa_cache_t cache, pisa_sequences_t seqs,
+                               void* stream);
+
+/*
+ * pisa_cache_read -- positions [0, min(kv_len, N)) of every sequence as bf16 [B, Hkv, N, d]
+ * (in 8 bits rounded once from code * scale). Rows behind a sequence's last are left as they
+ * were. q_lens is not used.
+ */
+pisa_status_t pisa_cache_read(pisa_cache_t cache, pisa_sequences_t seqs, void* K, void* V, void* stream);
+
+/* Bytes of device workspace that pisa_paged_attention needs (no device is touched). */
+pisa_status_t pisa_paged_attention_workspace(pisa_cache_t cache, pisa_sequences_t seqs, int32_t Hq,
+                                             pisa_window_t window, size_t* bytes);
+
+/*
+ * pisa_paged_attention -- the new tokens attend over their sequences in the cache (which
+ * holds the new tokens too), under the window. Q, O: bf16 [B, Hq, N, d]; lse: fp32
+ * [B, Hq, N] or NULL. Rows t >= q_len of O and lse are left as they were. workspace as in
+ * pisa_window_attention_backward (may be NULL if 0 bytes are needed).
+ */
+pisa_status_t pisa_paged_attention(const void* Q, pisa_cache_t cache, pisa_sequences_t seqs, int32_t Hq,
+                                   pisa_window_t window, float scale, void* O, float* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 /*
  * pisa_device_error -- takes the device error word that the kernels set, after all
  * work already enqueued on `stream`, and synchronises `stream`. Returns PISA_OK,
- * PISA_ERR_TIMEOUT (a bounded wait ran out), PISA_ERR_INVALID_ARG (an idx entry was out
- * of range) or PISA_ERR_CUDA.
+ * PISA_ERR_TIMEOUT (a bounded wait ran out), PISA_ERR_INVALID_ARG (an idx entry, a page or
+ * a length was out of range) or PISA_ERR_CUDA.
  * The word is ONE PER DEVICE, shared by every stream and host thread that uses the
  * library on the current device: a bit raised by a kernel on any stream is reported by
  * the first pisa_device_error() that takes the word after the bit was raised, whatever

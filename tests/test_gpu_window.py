@@ -1,0 +1,233 @@
+"""Windowed attention and its gradient on the GPU against the fp64 oracle."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import block_sparse_attention_pisa_b200 as P  # noqa: E402
+from oracle import window as W  # noqa: E402
+from tests import window_bounds as T  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+# (B, Hq, Hkv, N, d, left, right, sinks)
+SHAPES = [
+    (1, 1, 1, 1, 64, -1, 0, 0),            # one token
+    (1, 2, 1, 2, 128, 0, 0, 0),            # every token sees itself only
+    (1, 3, 1, 127, 64, -1, -1, 0),         # whole sequence, three heads per key head, odd length
+    (2, 4, 2, 128, 128, -1, 0, 0),         # causal, one tile
+    (1, 4, 4, 129, 64, 16, 0, 0),          # one token over a tile
+    (1, 2, 2, 257, 128, 5, 7, 3),          # both sides, odd reaches, sinks
+    (1, 8, 2, 300, 64, 31, 0, 1),          # sinks of one token
+    (1, 2, 1, 520, 128, 40, 0, 130),       # sinks over a tile's edge
+    (1, 5, 1, 401, 64, 64, 64, 0),         # group of five
+    (1, 7, 1, 200, 128, 20, 0, 4),         # group of seven: rows of a tile end inside a token
+    (2, 2, 2, 700, 64, 100, 0, 600),       # sinks longer than the window
+    (1, 2, 2, 384, 128, -1, 5, 0),         # no limit to the left, a few to the right
+    (1, 2, 1, 390, 64, 0, -1, 2),          # none before its own, all behind it
+    (3, 6, 3, 65, 128, 1000000000, 2000000000, 2000000000),  # reaches far past the end
+    (1, 16, 1, 150, 64, 33, 0, 8),         # sixteen heads on one key head
+    (1, 130, 1, 12, 64, 4, 0, 1),          # more heads of a group than rows of a tile
+]
+
+
+def make(B, Hq, Hkv, N, d, seed=0, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    new = lambda h, s=1.0: (torch.randn(B, h, N, d, generator=g) * s).to(torch.bfloat16).cuda()  # noqa: E731
+    return new(Hq, spread), new(Hkv, spread), new(Hkv), new(Hq)
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def check_forward(O, lse, Q, K, V, left, right, sinks, scale, heads=None):
+    q, k, v, o, l = (f64(t) for t in (Q, K, V, O, lse))
+    B, Hq, N, _ = q.shape
+    G = Hq // k.shape[1]
+    see = W.visible(np.arange(N), N, left, right, sinks)
+    want = np.zeros_like(q)
+    for b in range(B):
+        for h in range(Hq) if heads is None else heads:
+            want[b, h], wl, to, tl = T.forward(q[b, h], k[b, h // G], v[b, h // G], see, scale)
+            T.check(o[b, h], want[b, h], to, f"O[{b},{h}]")
+            T.check(l[b, h], wl, tl, f"lse[{b},{h}]")
+    if heads is None:
+        T.check_norm(o, want, "O")
+
+
+def check_backward(grads, dO, Q, K, V, left, right, sinks, scale, norms=True):
+    do, q, k, v = (f64(t) for t in (dO, Q, K, V))
+    dQ, dK, dV = (f64(t) for t in grads)
+    B, Hq, N, _ = q.shape
+    G = Hq // k.shape[1]
+    see = W.visible(np.arange(N), N, left, right, sinks)
+    wq, tq = np.zeros_like(q), np.zeros_like(q)
+    wk, wv, tk, tv = (np.zeros_like(k) for _ in range(4))
+    for b in range(B):
+        for h in range(Hq):
+            dq, dk, dv, a, c, e = T.backward(do[b, h], q[b, h], k[b, h // G], v[b, h // G], see, scale)
+            wq[b, h], tq[b, h] = dq, a
+            wk[b, h // G] += dk
+            wv[b, h // G] += dv
+            tk[b, h // G] += c
+            tv[b, h // G] += e
+    T.check(dQ, wq, tq, "dQ")
+    T.check(dK, wk, tk + T.U * np.abs(wk) * T.SLACK, "dK")
+    T.check(dV, wv, tv + T.U * np.abs(wv) * T.SLACK, "dV")
+    if norms:
+        for got, want, name in ((dQ, wq, "dQ"), (dK, wk, "dK"), (dV, wv, "dV")):
+            T.check_norm(got, want, name)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward_and_gradient(shape):
+    B, Hq, Hkv, N, d, left, right, sinks = shape
+    Q, K, V, dO = make(B, Hq, Hkv, N, d, seed=N)
+    mask = dict(left=left, right=right, sinks=sinks)
+    O, lse = P.window_attention(Q, K, V, **mask)
+    P.device_error()
+    check_forward(O, lse, Q, K, V, left, right, sinks, d ** -0.5)
+    grads = P.window_attention_backward(dO, Q, K, V, O, lse, **mask)
+    P.device_error()
+    # with few keys per row ds cancels: dQ, dK are small beside what their roundings are relative to
+    check_backward(grads, dO, Q, K, V, left, right, sinks, d ** -0.5, norms=N > 100)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_scale_and_large_scores(d):
+    """Scores of several hundred: the running maximum moves by much more than one rescale step."""
+    Q, K, V, dO = make(1, 2, 1, 333, d, seed=5, spread=6.0)
+    mask = dict(left=150, right=0, sinks=10, scale=0.5)
+    O, lse = P.window_attention(Q, K, V, **mask)
+    check_forward(O, lse, Q, K, V, 150, 0, 10, 0.5)
+    check_backward(P.window_attention_backward(dO, Q, K, V, O, lse, **mask), dO, Q, K, V, 150, 0, 10, 0.5, norms=False)
+
+
+def test_growing_scores_rescale():
+    """Keys grow along the sequence, so every tile raises the maximum."""
+    Q, K, V, dO = make(1, 1, 1, 600, 64, seed=6)
+    ramp = torch.linspace(0, 20, 600, device="cuda")[None, None, :, None]
+    K = (K.float() * 0.1 + ramp * 0.2).to(torch.bfloat16)
+    Q = (Q.float() * 0.1 + 1).to(torch.bfloat16)
+    O, lse = P.window_attention(Q, K, V)
+    check_forward(O, lse, Q, K, V, -1, -1, 0, 64 ** -0.5)
+    check_backward(P.window_attention_backward(dO, Q, K, V, O, lse), dO, Q, K, V, -1, -1, 0, 64 ** -0.5, norms=False)
+
+
+def test_long_sequence_last_rows():
+    """A long sequence: the last rows against the oracle on the keys they see."""
+    N, left, sinks = 20011, 300, 40
+    Q, K, V, _ = make(1, 2, 1, N, 128, seed=7)
+    O, lse = P.window_attention(Q, K, V, left=left, right=0, sinks=sinks)
+    q, k, v = f64(Q), f64(K), f64(V)
+    rows = np.arange(N - 200, N)
+    see = W.visible(rows, N, left, 0, sinks)
+    for h in range(2):
+        o, l, to, tl = T.forward(q[0, h, rows], k[0, 0], v[0, 0], see, 128 ** -0.5)
+        T.check(f64(O)[0, h, rows], o, to, "O")
+        T.check(f64(lse)[0, h, rows], l, tl, "lse")
+
+
+def test_gradient_against_differences():
+    """<dX, direction> against the change of the loss along it, both from the kernel's own forward
+    call on a smooth problem: forward differences in O of size eps, O to bf16."""
+    N, d = 260, 64
+    Q, K, V, dO = make(1, 2, 1, N, d, seed=8)
+    mask = dict(left=90, right=0, sinks=5)
+    O, lse = P.window_attention(Q, K, V, **mask)
+    grads = P.window_attention_backward(dO, Q, K, V, O, lse, **mask)
+    see = W.visible(np.arange(N), N, 90, 0, 5)
+    do = f64(dO)
+
+    def loss(q, k, v):
+        return sum((W.attend(q[0, h], k[0, 0], v[0, 0], see, d ** -0.5)[0] * do[0, h]).sum() for h in range(2))
+
+    rng = np.random.default_rng(9)
+    base = [f64(Q), f64(K), f64(V)]
+    for i, g in enumerate(grads):
+        # along the gradient's own direction the product is its norm: no cancellation
+        way = f64(g) + 0.1 * np.abs(f64(g)).mean() * rng.normal(size=base[i].shape)
+        way /= np.linalg.norm(way)
+        eps = 1e-4
+        up, down = ([x + s * eps * way if k == i else x for k, x in enumerate(base)] for s in (1, -1))
+        want = (loss(*up) - loss(*down)) / (2 * eps)
+        got = float((f64(g) * way).sum())
+        assert abs(got - want) <= T.U * abs(want)
+
+
+def test_same_bits_and_head_alone():
+    """The same call gives the same bits, and a head alone gives the bits it has in a batch."""
+    shape = (2, 6, 2, 777, 128)
+    Q, K, V, dO = make(*shape, seed=11)
+    mask = dict(left=200, right=0, sinks=30)
+    first = [*P.window_attention(Q, K, V, **mask)]
+    first += P.window_attention_backward(dO, Q, K, V, *first, **mask)
+    for _ in range(3):
+        again = [*P.window_attention(Q, K, V, **mask)]
+        again += P.window_attention_backward(dO, Q, K, V, *again, **mask)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+    q, k, v, do = Q[1:, 3:], K[1:, 1:], V[1:, 1:], dO[1:, 3:]
+    q, k, v, do = (t.contiguous() for t in (q, k, v, do))
+    alone = [*P.window_attention(q, k, v, **mask)]
+    assert torch.equal(alone[0], first[0][1:, 3:]) and torch.equal(alone[1], first[1][1:, 3:])
+    alone += P.window_attention_backward(do, q, k, v, *alone, **mask)
+    for a, b, h in zip(alone[2:], first[2:], (3, 1, 1)):
+        assert torch.equal(a, b[1:, h:])
+
+
+def test_outputs_given_streams_and_graph():
+    """Preallocated outputs and workspace, a stream of its own, and a captured step replayed on
+    new inputs give the bits of plain calls."""
+    B, Hq, Hkv, N, d = 1, 4, 2, 333, 64
+    Q, K, V, dO = make(B, Hq, Hkv, N, d, seed=12)
+    mask = dict(left=70, right=3, sinks=9)
+    outs = [torch.empty_like(Q), torch.empty(B, Hq, N, device="cuda"), torch.empty_like(Q), torch.empty_like(K),
+            torch.empty_like(V)]
+    ws = torch.empty(P.window_attention_backward_workspace(B, Hq, Hkv, N, d, **mask), dtype=torch.uint8, device="cuda")
+
+    def step():
+        P.window_attention(Q, K, V, out=outs[0], lse=outs[1], **mask)
+        P.window_attention_backward(dO, Q, K, V, outs[0], outs[1], out=outs[2:], workspace=ws, **mask)
+
+    want = [*P.window_attention(Q, K, V, **mask)]
+    want += P.window_attention_backward(dO, Q, K, V, *want, **mask)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    new = make(B, Hq, Hkv, N, d, seed=13)
+    for t, x in zip((Q, K, V, dO), new):
+        t.copy_(x)
+    ws.fill_(255)  # nothing of an earlier call is needed: the bytes read as NaN
+    g.replay()
+    torch.cuda.synchronize()
+    want = [*P.window_attention(*new[:3], **mask)]
+    want += P.window_attention_backward(new[3], *new[:3], *want, **mask)
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    P.device_error()
+
+
+def test_infinities_and_nan_stay_in_their_sequence_and_head():
+    """A NaN in one head's keys reaches that key head's rows only; the other heads keep their bits."""
+    Q, K, V, _ = make(2, 4, 2, 200, 64, seed=14)
+    want, _ = P.window_attention(Q, K, V, left=50, right=0)
+    bad = K.clone()
+    bad[1, 0, 120] = float("nan")
+    O, lse = P.window_attention(Q, bad, V, left=50, right=0)
+    assert torch.equal(O[0], want[0]) and torch.equal(O[1, 2:], want[1, 2:])
+    assert torch.equal(O[1, :2, :120], want[1, :2, :120])
+    assert torch.isnan(O[1, :2, 120:171].float()).all() and torch.isnan(lse[1, :2, 120:171]).all()
+    assert torch.equal(O[1, :2, 171:], want[1, :2, 171:])
+
+
+def test_empty_problem():
+    Q = torch.empty(0, 2, 5, 64, dtype=torch.bfloat16, device="cuda")
+    O, lse = P.window_attention(Q, Q, Q)
+    assert O.shape == Q.shape and lse.shape == (0, 2, 5)
+    assert [g.shape for g in P.window_attention_backward(Q, Q, Q, Q, O, lse)] == [Q.shape] * 3
