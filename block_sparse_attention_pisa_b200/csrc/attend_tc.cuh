@@ -1,0 +1,578 @@
+// Attention under a token-exact window on the tensor cores (tcgen05 / TMEM / TMA), over keys
+// laid out plainly or in pages.
+//
+//   o = sum_j exp(s_j - m) v_j / l,  l = sum_j exp(s_j - m),  s_j = scale q.k_j, j visible
+//
+// one pass over the keys with a running maximum m and sum l per row. The rows of a key head
+// are its G = Hq / Hkv query heads' tokens, token-major (row r = token r / G, head r % G), so
+// that shared keys are read once for all of them and a tile of rows spans few positions.
+//
+// A CTA takes two tiles (groups) of 128 rows of one key head and walks the 128-key tiles that
+// some row of theirs sees (the tiles of the first tokens, then the window's); a group skips
+// the ones that none of its rows sees. Warp roles:
+//   warp 0       producer: K and V tiles by TMA (a page at a time in a paged cache) into a ring;
+//   warp 1       one thread issues every tcgen05.mma: per tile and group S = Q K^T (SS), then
+//                O += P V (TS, P from tensor memory);
+//   warps 2-3    paged caches: clear the rows of a V tile that no row may see (unwritten rows
+//                may hold anything, and 0 x NaN is NaN); 8 bits: convert codes to bf16;
+//   warps 4-11   softmax: one thread per row (group = warps 4-7 or 8-11).
+// Tensor memory: S of either group (128 columns each, P in bf16 over the first half of its own
+// S) and O of either group (D columns each).
+//
+// The two groups alternate on the tensor core: while one group's exponentials run, the other's
+// P V and next Q K^T do. Products are issued by one thread and execute in order, so S of tile
+// i + 1 may overwrite P of tile i behind the P V that reads it, and a group that sees its S(i + 1)
+// (one commit) knows its O holds the products up to tile i: O is rescaled without a further
+// wait. The accumulator is rescaled only when the maximum grows by more than 2^8.
+//
+// Bound: at D = 128 a tile of 128 x 128 takes 2 x 512 cycles of tensor time and as long on the
+// exponential unit (16 per cycle and SM); at D = 64 the exponentials are twice the products.
+#pragma once
+
+#include "attention_tc.cuh"
+#include "window.cuh"
+
+namespace pisa {
+
+struct AttendTcParams {
+  const bf16* Q;
+  bf16* O;
+  float* lse;
+  float* part;      // splits > 1: fp32 [splits][B * Hq * N][D], then base-2 lse [splits][B * Hq * N]
+  float* part_lse;
+  Pages pages;      // paged only
+  int B, Hq, Hkv, N;
+  int pairs;        // CTAs along a key head's rows
+  int splits;       // runs that a CTA's tile list is cut into
+  Window win;
+  float scale;
+};
+
+template <int D, int KV>
+struct AttendTcCfg {
+  static constexpr int kThreads = 384;
+  static constexpr bool CODES = KV == kKvPagedE4m3;
+  static constexpr int TILE = 128 * D * 2;          // bytes of a 128-row bf16 tile
+  static constexpr int NS = CODES ? 3 : (D == 128 ? 5 : 10);  // ring stages
+  static constexpr int NL = CODES ? (D == 128 ? 3 : 6) : NS;  // landing stages (8 bits: tiles of codes)
+  static constexpr int LAND = CODES ? 128 * D : 0;  // bytes of a landing stage of its own
+  static constexpr int OFF_Q = 0;                   // two groups' queries
+  static constexpr int OFF_RING = 2 * TILE;
+  static constexpr int OFF_CODES = OFF_RING + NS * TILE;
+  static constexpr int OFF_SCALE = OFF_CODES + NL * LAND;  // 8 bits: float [8 warps][K, V][128]
+  static constexpr int B_FULL = 0;                  // [NS] stage holds its tile
+  static constexpr int B_EMPTY = B_FULL + NS;       // [NS] products that read it are done (commit)
+  static constexpr int B_LAND = B_EMPTY + NS;       // [NL] paged: copies landed, rows not cleared yet
+  static constexpr int B_LEMPTY = B_LAND + NL;      // [NL] 8 bits: codes converted (2 warps)
+  static constexpr int B_Q = B_LEMPTY + NL;         // [2] a group's queries are in shared memory
+  static constexpr int B_S = B_Q + 2;               // [2] S ready (commit)
+  static constexpr int B_P = B_S + 2;               // [2] P written (4 warps)
+  static constexpr int B_O = B_P + 2;               // all products done (commit)
+  static constexpr int NBARS = B_O + 1;
+  static constexpr int OFF_BAR = OFF_SCALE + (CODES ? 8 * 2 * 128 * 4 : 0);
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NBARS;
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static constexpr int S_COL = 0, O_COL = 256;
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+};
+
+// What a group of rows sees: sinks [0, sk) and window [lo, hi); rows at positions p0 .. p1.
+struct Sight {
+  int p0, p1, lo, hi, sk;
+  __device__ __forceinline__ void set(const Window& w, int first, int last, int n) {
+    p0 = first;
+    p1 = last;
+    hi = max(0, min(n, last + w.right + 1));
+    lo = min(hi, max(0, first - w.left));
+    sk = min(w.sinks, hi);
+  }
+  __device__ __forceinline__ void none() { p0 = p1 = lo = hi = sk = 0; }
+  // some row may see a key of [j0, j0 + 128)
+  __device__ __forceinline__ bool any(int j0) const { return j0 < sk || (j0 < hi && j0 + 128 > lo); }
+  // some row may see a key of [j0, j0 + w)
+  __device__ __forceinline__ bool any(int j0, int w) const { return j0 < sk || (j0 < hi && j0 + w > lo); }
+};
+
+// The tiles of 128 keys that two groups see together, split into runs.
+struct TileList {
+  int ns, first, from, to;  // sink tiles before the window's, window's first tile, this run
+  __device__ __forceinline__ void set(const Sight& a, int split, int splits) {
+    const int w0 = a.lo >> 7, w1 = a.hi > a.lo ? (a.hi + 127) >> 7 : w0;
+    ns = min((a.sk + 127) >> 7, w0);
+    first = w0;
+    const long long total = ns + (w1 - w0);
+    from = int(total * split / splits);
+    to = int(total * (split + 1) / splits);
+  }
+  __device__ __forceinline__ int key(int i) const { return (i < ns ? i : first + i - ns) << 7; }
+};
+
+__device__ __forceinline__ uint32_t ones_below(int k) {  // bits [0, k) of a word, any k
+  return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u);
+}
+
+// pages of the tile at j0 that `a` may see and the table holds: bit i = page i of the tile
+__device__ __forceinline__ uint32_t held_pages(const Pages& g, int b, const Sight& a, int j0, int lane) {
+  const int per = 128 >> g.log_page;
+  bool ok = false;
+  if (lane < per) {
+    const int j = j0 + (lane << g.log_page);
+    ok = a.any(j, 1 << g.log_page) && page_of(g, b, j) >= 0;
+  }
+  return __ballot_sync(0xffffffffu, ok);
+}
+
+template <int D, int KV>
+__global__ void __launch_bounds__(384, 1)
+attend_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const AttendTcParams p) {
+  using C = AttendTcCfg<D, KV>;
+  using namespace tc;
+  extern __shared__ __align__(16) uint8_t attend_smem[];
+  const uint32_t raw_u = smem_u32(attend_smem);
+  const uint32_t base_u = (raw_u + 1023u) & ~1023u;
+  uint8_t* base = attend_smem + (base_u - raw_u);
+  volatile int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC) + 1;
+  const uint32_t bar0 = base_u + C::OFF_BAR;
+#define ABAR(i) (bar0 + 8u * uint32_t(i))
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- which rows, which keys: the same for every thread
+  const int G = p.Hq / p.Hkv;
+  int id = blockIdx.x;
+  const int pair = p.pairs - 1 - id % p.pairs;  // causal: the rows with the most keys first
+  id /= p.pairs;
+  const int split = id % p.splits, bh = id / p.splits;
+  const int b = bh / p.Hkv, hk = bh % p.Hkv;
+  int n = p.N, nq = p.N;
+  if constexpr (KV != kKvPlain) {
+    n = kv_len_of(p.pages, b);
+    nq = q_len_of(p.pages, b, p.N);
+  }
+  const int rows = nq * G;  // fits: B * Hq * N does
+  const int row0 = pair * 256;
+  if (row0 >= rows) return;
+  Sight see[2], both;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int a = row0 + 128 * g, z = min(a + 127, rows - 1);
+    if (a < rows) see[g].set(p.win, n - nq + a / G, n - nq + z / G, n);
+    else see[g].none();
+  }
+  both = see[0];
+  if (see[1].hi > 0) {
+    both.lo = see[0].hi > 0 ? min(see[0].lo, see[1].lo) : see[1].lo;
+    both.hi = max(see[0].hi, see[1].hi);
+    both.sk = max(see[0].sk, see[1].sk);
+  }
+  TileList tiles;
+  tiles.set(both, split, p.splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(ABAR(C::B_FULL + s), C::CODES ? 2 : 1);
+      mbar_init(ABAR(C::B_EMPTY + s), 1);
+    }
+    for (int s = 0; s < C::NL; ++s) {
+      mbar_init(ABAR(C::B_LAND + s), 1);
+      mbar_init(ABAR(C::B_LEMPTY + s), 2);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(ABAR(C::B_Q + g), 4);
+      mbar_init(ABAR(C::B_S + g), 1);
+      mbar_init(ABAR(C::B_P + g), 4);
+    }
+    mbar_init(ABAR(C::B_O), 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 2) {
+    tmem_alloc(base_u + C::OFF_MISC, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- producer
+    // Lanes 0 and 1 issue the two 64-column panels of a tile (D = 64: lane 0 alone); stage use
+    // 2 i holds K of the run's i-th tile, 2 i + 1 its V.
+    if (lane < 2) {
+      bool ok = true;
+      int use = 0;
+      for (int i = tiles.from; i < tiles.to && ok; ++i) {
+        const int j0 = tiles.key(i);
+        for (int kv = 0; kv < 2 && ok; ++kv, ++use) {
+          // the stage that the copies land in: the ring's, or one for codes
+          constexpr int NL = C::NL;
+          const int s = use % NL;
+          ok = wait_bounded(ABAR((C::CODES ? C::B_LEMPTY : C::B_EMPTY) + s), ((use / NL) & 1) ^ 1, abort_flag);
+          ok = __all_sync(0x3u, ok);
+          if (!ok) break;
+          const uint32_t dst = base_u + (C::CODES ? C::OFF_CODES + s * C::LAND : C::OFF_RING + s * C::TILE);
+          if constexpr (KV == kKvPlain) {
+            if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_FULL + s), C::TILE);
+            __syncwarp(0x3u);
+            if (lane * 64 < D)
+              tma_load_3d(dst + lane * 16384, kv ? &tmV : &tmK, ABAR(C::B_FULL + s), lane * 64, j0, bh);
+          } else {
+            // pages that no row of the CTA sees, or that the table does not hold, stay out
+            const int per = 128 >> p.pages.log_page, size = 1 << p.pages.log_page;
+            uint32_t held = 0;
+            for (int q = 0; q < per; ++q)
+              if (both.any(j0 + q * size, size) && page_of(p.pages, b, j0 + q * size) >= 0) held |= 1u << q;
+            if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_LAND + s), __popc(held) * size * D * (C::CODES ? 1 : 2));
+            __syncwarp(0x3u);
+            if constexpr (C::CODES) {  // whole rows of D codes, lanes by turns
+              for (int q = lane; q < per; q += 2)
+                if ((held >> q) & 1u)
+                  tma_load_3d(dst + q * size * D, kv ? &tmV : &tmK, ABAR(C::B_LAND + s), 0, 0,
+                              page_of(p.pages, b, j0 + q * size) * p.Hkv + hk);
+            } else if (lane * 64 < D) {
+              for (int q = 0; q < per; ++q)
+                if ((held >> q) & 1u)
+                  tma_load_3d(dst + lane * 16384 + q * size * 128, kv ? &tmV : &tmK, ABAR(C::B_LAND + s), lane * 64, 0,
+                              page_of(p.pages, b, j0 + q * size) * p.Hkv + hk);
+            }
+          }
+        }
+      }
+      // no copy may still be in flight when the CTA exits
+      constexpr int landed = KV == kKvPlain ? C::B_FULL : C::B_LAND;
+      if (lane == 0)
+        for (int u = use > C::NL ? use - C::NL : 0; u < use; ++u) wait_drain(ABAR(landed + u % C::NL), (u / C::NL) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16(128, 128, false), idO = idesc_bf16(128, D, true);
+      bool ok = true;
+      uint32_t has_o = 0, n_p = 0;  // bit g: O holds a product; phase of P
+      auto stage = [&](int use) { return base_u + C::OFF_RING + (use % C::NS) * C::TILE; };
+      auto full = [&](int use) { return wait_poll(ABAR(C::B_FULL + use % C::NS), (use / C::NS) & 1, abort_flag); };
+      auto scores = [&](int g, int i) {  // S = Q K^T of the run's i-th tile
+        const uint32_t q = base_u + C::OFF_Q + g * C::TILE, k = stage(2 * i);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint32_t off = (c >> 2) * 16384 + (c & 3) * 32;
+          umma_ss(tmem + C::S_COL + g * 128, sdesc_sw128(q + off, 16, 1024), sdesc_sw128(k + off, 16, 1024), idS,
+                  c ? 1u : 0u);
+        }
+        umma_commit(ABAR(C::B_S + g));
+      };
+      auto values = [&](int g, int i) {  // O += P V
+        const uint32_t v = stage(2 * i + 1);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          umma_ts(tmem + C::O_COL + g * D, tmem + C::S_COL + g * 128 + c * 8, sdesc_sw128(v + c * 2048, 16384, 1024), idO,
+                  (((has_o >> g) & 1u) | uint32_t(c)) ? 1u : 0u);
+        has_o |= 1u << g;
+      };
+      const int count = tiles.to - tiles.from;
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (see[g].hi > 0 && ok) ok = wait_poll(ABAR(C::B_Q + g), 0, abort_flag);
+      for (int i = -1; i < count && ok; ++i) {
+        const bool more = i + 1 < count;
+        const int j = i >= 0 ? tiles.key(tiles.from + i) : 0, jn = more ? tiles.key(tiles.from + i + 1) : 0;
+        bool have_v = false, have_k = false;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (i >= 0 && see[g].any(j)) {
+            if (!have_v && !(ok = full(2 * i + 1))) break;
+            have_v = true;
+            if (!(ok = wait_poll(ABAR(C::B_P + g), (n_p >> g) & 1u, abort_flag))) break;
+            n_p ^= 1u << g;
+            tc_fence_after();
+            values(g, i);
+          }
+          if (more && see[g].any(jn)) {
+            if (!have_k && !(ok = full(2 * i + 2))) break;
+            have_k = true;
+            tc_fence_after();
+            scores(g, i + 1);
+          }
+        }
+        if (!ok) break;
+        // a tile of the list is seen by one group at least, so its copies have been awaited
+        if (i >= 0) umma_commit(ABAR(C::B_EMPTY + (2 * i + 1) % C::NS));
+        if (more) umma_commit(ABAR(C::B_EMPTY + (2 * i + 2) % C::NS));
+      }
+      umma_commit(ABAR(C::B_O));
+      wait_drain(ABAR(C::B_O), 0);  // nothing of ours may run on after the CTA frees TMEM
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------- paged: rows nobody may see
+    if constexpr (KV == kKvPagedE4m3) {
+      // 16 codes per thread and step -> 32 bytes of the swizzled operand; rows that nobody may
+      // see become zero. The scales stay out: scores and weights take them exactly in fp32.
+      const int count = tiles.to - tiles.from, ct = threadIdx.x - 64;
+      constexpr int CH = D / 16;  // 16-code chunks of a row
+      for (int u = 0; u < 2 * count; ++u) {
+        const int sl = u % C::NL, s = u % C::NS, j0 = tiles.key(tiles.from + (u >> 1));
+        const uint32_t held = held_pages(p.pages, b, both, j0, lane);
+        bool ok = wait_bounded(ABAR(C::B_EMPTY + s), ((u / C::NS) & 1) ^ 1, abort_flag) &&
+                  wait_bounded(ABAR(C::B_LAND + sl), (u / C::NL) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll 4
+        for (int x = ct; x < 128 * CH; x += 64) {
+          const int r = x / CH, c = x % CH, j = j0 + r;
+          uint4 code = *reinterpret_cast<const uint4*>(base + C::OFF_CODES + sl * C::LAND + r * D + c * 16);
+          const bool in = ((held >> (r >> p.pages.log_page)) & 1u) && (j < both.sk || (j >= both.lo && j < both.hi));
+          if (!in) code = make_uint4(0, 0, 0, 0);
+          const uint4 lo = make_uint4(e4m3x2_to_bf16x2(code.x), e4m3x2_to_bf16x2(code.x >> 16),
+                                      e4m3x2_to_bf16x2(code.y), e4m3x2_to_bf16x2(code.y >> 16));
+          const uint4 hi = make_uint4(e4m3x2_to_bf16x2(code.z), e4m3x2_to_bf16x2(code.z >> 16),
+                                      e4m3x2_to_bf16x2(code.w), e4m3x2_to_bf16x2(code.w >> 16));
+          uint8_t* dst = base + C::OFF_RING + s * C::TILE + (c >> 2) * 16384 + r * 128;
+          const int c0 = (2 * c) & 7;
+          *reinterpret_cast<uint4*>(dst + ((c0 ^ (r & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = hi;
+        }
+        fence_proxy_async_smem();
+        warp_arrive(ABAR(C::B_FULL + s));
+        warp_arrive(ABAR(C::B_LEMPTY + sl));
+      }
+    } else if constexpr (KV == kKvPaged) {
+      if (warp == 2) {
+        const int count = tiles.to - tiles.from;
+        for (int u = 0; u < 2 * count; ++u) {
+          const int s = u % C::NS, j0 = tiles.key(tiles.from + (u >> 1));
+          if (!__all_sync(0xffffffffu, wait_bounded(ABAR(C::B_LAND + s), (u / C::NS) & 1, abort_flag))) break;
+          if (u & 1) {
+            const uint32_t held = held_pages(p.pages, b, both, j0, lane);
+            for (int r = lane; r < 128; r += 32) {
+              const int j = j0 + r;
+              const bool in = ((held >> (r >> p.pages.log_page)) & 1u) && (j < both.sk || (j >= both.lo && j < both.hi));
+              if (!in)
+                for (int pn = 0; pn < D / 64; ++pn)
+#pragma unroll
+                  for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(base + C::OFF_RING + s * C::TILE + pn * 16384 + r * 128 + c * 16) =
+                        make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+          warp_arrive(ABAR(C::B_FULL + s));
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int g = (warp - 4) >> 2;
+    const Sight mine = g ? see[1] : see[0];
+    const int r = row0 + 128 * g + (threadIdx.x & 127);
+    const uint32_t lrow = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lrow + C::S_COL + g * 128, o_addr = tmem + lrow + C::O_COL + g * D;
+    const bool real = r < rows;
+    const int t = real ? r / G : 0, head = hk * G + (real ? r % G : 0);
+    const size_t row = (size_t(b) * p.Hq + head) * p.N + t;
+    const int pos = n - nq + t;
+    bool ok = true;
+    if (mine.hi > 0) {
+      // this row's query into the 128-byte swizzled operand
+      const uint4* src = reinterpret_cast<const uint4*>(p.Q + row * D);
+      const int rt = threadIdx.x & 127;
+      uint8_t* dst = base + C::OFF_Q + g * C::TILE + rt * 128;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (rt & 7)) << 4)) =
+            real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      warp_arrive(ABAR(C::B_Q + g));
+    }
+    const float sl2 = p.scale * 1.4426950408889634f;
+    // the keys this row sees: up to z, and from a on or below the sinks' end
+    const int z = max(-1, min(n - 1, pos + p.win.right)), a = max(0, pos - p.win.left);
+    // 8 bits: a warp keeps its tile's scales in shared memory, the next tile's in registers
+    float4 next_k, next_v;
+    float* scales = reinterpret_cast<float*>(base + C::OFF_SCALE) + (C::CODES ? (warp - 4) * 256 : 0);
+    auto fetch_scales = [&](int i) {
+      next_k = next_v = make_float4(0.f, 0.f, 0.f, 0.f);  // keys that nobody may see weigh nothing
+      while (i < tiles.to && !mine.any(tiles.key(i))) ++i;
+      if (i >= tiles.to) return;
+      const int j = tiles.key(i) + 4 * lane, page = p.pages.table[size_t(b) * p.pages.max_pages + min(j, n - 1) / (1 << p.pages.log_page)];
+      const bool in = mine.any(j, 4) && page >= 0 && page < p.pages.num_pages;
+      if (!in) return;
+      const size_t at = ((size_t(page) * p.Hkv + hk) << p.pages.log_page) + (j & ((1 << p.pages.log_page) - 1));
+      next_k = __ldg(reinterpret_cast<const float4*>(p.pages.ks + at));
+      next_v = __ldg(reinterpret_cast<const float4*>(p.pages.vs + at));
+      float* f = reinterpret_cast<float*>(&next_v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (!(j + k < mine.sk || (j + k >= mine.lo && j + k < mine.hi))) f[k] = 0.f;
+    };
+    if constexpr (C::CODES) fetch_scales(tiles.from);
+    float m = -INFINITY, l = 0.f;
+    uint32_t phase = 0, done = 0;
+    for (int i = tiles.from; i < tiles.to; ++i) {
+      const int j0 = tiles.key(i);
+      if (!mine.any(j0)) continue;
+      uint32_t held = 0xffu;
+      if constexpr (KV != kKvPlain) held = held_pages(p.pages, b, mine, j0, lane);
+      const bool whole = j0 + 127 <= mine.p0 + p.win.right && j0 + 128 <= n &&
+                         (j0 >= mine.p1 - p.win.left || j0 + 128 <= p.win.sinks) &&
+                         (KV == kKvPlain || held == (1u << (128 >> p.pages.log_page)) - 1u);
+      if constexpr (C::CODES) {
+        __syncwarp();  // the previous tile's scales have been read
+        reinterpret_cast<float4*>(scales)[lane] = next_k;
+        reinterpret_cast<float4*>(scales + 128)[lane] = next_v;
+        __syncwarp();
+        fetch_scales(i + 1);
+        __syncwarp();
+      }
+      ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_S + g), phase, abort_flag));
+      if (!ok) break;
+      phase ^= 1u;
+      tc_fence_after();
+      uint32_t sc[128];
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch) tmem_ld16(s_addr + ch * 16, *reinterpret_cast<uint32_t(*)[16]>(&sc[ch * 16]));
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch) tmem_wait_ld(*reinterpret_cast<uint32_t(*)[16]>(&sc[ch * 16]));
+      if constexpr (C::CODES) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float4 f = reinterpret_cast<const float4*>(scales)[k];
+          sc[4 * k] = __float_as_uint(__uint_as_float(sc[4 * k]) * f.x);
+          sc[4 * k + 1] = __float_as_uint(__uint_as_float(sc[4 * k + 1]) * f.y);
+          sc[4 * k + 2] = __float_as_uint(__uint_as_float(sc[4 * k + 2]) * f.z);
+          sc[4 * k + 3] = __float_as_uint(__uint_as_float(sc[4 * k + 3]) * f.w);
+        }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t bits = ones_below(z - j0 + 1 - 32 * w) &
+                          (~ones_below(a - j0 - 32 * w) | ones_below(p.win.sinks - j0 - 32 * w));
+          if constexpr (KV != kKvPlain) {
+            // 32 keys are one page of 32, a part of a larger one, or two of 16
+            if (p.pages.log_page >= 5) bits = ((held >> ((32 * w) >> p.pages.log_page)) & 1u) ? bits : 0u;
+            else bits &= ((held >> (2 * w)) & 1u ? 0xffffu : 0u) | ((held >> (2 * w + 1)) & 1u ? 0xffff0000u : 0u);
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!((bits >> k) & 1u)) sc[32 * w + k] = __float_as_uint(-INFINITY);
+        }
+      }
+      float mxp[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mxp[k] = __uint_as_float(sc[k]);
+#pragma unroll
+      for (int k = 8; k < 128; ++k) mxp[k & 7] = fmaxf(mxp[k & 7], __uint_as_float(sc[k]));
+      const float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
+                             fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7]))) * sl2;
+      const bool grow = mx > m + 8.f;
+      const bool move = grow && m != -INFINITY;
+      if (__any_sync(0xffffffffu, move)) {  // S(i) is behind every earlier product of the group
+        const float f = move ? ex2(m - mx) : 1.f;
+        rescale_row<D>(o_addr, f);
+        l *= f;
+      }
+      if (grow) m = mx;
+      const float negm = m == -INFINITY ? 0.f : -m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float e0 = ex2(fmaf(__uint_as_float(sc[ch * 32 + 2 * k]), sl2, negm));
+          const float e1 = ex2(fmaf(__uint_as_float(sc[ch * 32 + 2 * k + 1]), sl2, negm));
+          sum[k & 3] += e0 + e1;
+          if constexpr (C::CODES) {  // the value's scale may be NaN, or the weight huge beside it
+            const float2 f = reinterpret_cast<const float2*>(scales + 128)[ch * 16 + k];
+            pk[k] = pack_bf16x2(e0 * f.x, e1 * f.y);
+          } else {
+            pk[k] = pack_bf16x2_int(e0, e1);
+          }
+        }
+        tmem_st16(s_addr + ch * 16, pk);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(ABAR(C::B_P + g));
+      done = 1;
+    }
+    ok = __all_sync(0xffffffffu, ok && wait_bounded(ABAR(C::B_O), 0, abort_flag));
+    tc_fence_after();
+    const float inv = l != 0.f ? 1.f / l : 0.f;  // l is NaN if a score was
+    const bool split_out = p.splits > 1;
+    const size_t at = size_t(split) * size_t(p.B) * p.Hq * p.N + row;
+#pragma unroll 1
+    for (int ch = 0; ch < D / 16; ++ch) {
+      __syncwarp();
+      uint32_t o[16];
+      if (done) {
+        tmem_ld16(o_addr + ch * 16, o);
+        tmem_wait_ld(o);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = 0u;
+      }
+      if (!real || !ok) continue;
+      if (split_out) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          reinterpret_cast<float4*>(p.part + at * D + ch * 16)[k] =
+              make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
+                          __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
+      } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          w[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+        uint4* dst = reinterpret_cast<uint4*>(p.O + row * D + ch * 16);
+        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+    if (real && ok) {
+      const float lg = l != 0.f ? m + __log2f(l) : -INFINITY;
+      if (split_out) p.part_lse[at] = lg;
+      else if (p.lse) p.lse[row] = lg * 0.6931471805599453f;
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+#undef ABAR
+}
+
+// Joins the runs of a row: weights 2^(lse_s - max), in run order. One warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) attend_join_kernel(const AttendTcParams p, int paged) {
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = int64_t(p.B) * p.Hq * p.N, row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  if (paged) {
+    const int b = int(row / (int64_t(p.Hq) * p.N)), t = int(row % p.N);
+    if (t >= q_len_of(p.pages, b, p.N)) return;
+  }
+  float m = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.part_lse[s * rows + row]);
+  const float m0 = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float w = tc::ex2(p.part_lse[s * rows + row] - m0);
+    if (w == 0.f) continue;
+    l += w;
+    const float* src = p.part + (s * rows + row) * D;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = fmaf(w, src[i * 32 + lane], o[i]);
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) p.O[row * D + i * 32 + lane] = __float2bfloat16(o[i] * inv);
+  if (lane == 0 && p.lse) p.lse[row] = l != 0.f ? (m0 + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+}  // namespace pisa

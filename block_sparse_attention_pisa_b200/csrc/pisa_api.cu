@@ -20,6 +20,7 @@
 #include "host_pipeline.cuh"
 #include "cache.cuh"
 #include "window_attention.cuh"
+#include "attend_tc.cuh"
 
 using pisa::bf16;
 

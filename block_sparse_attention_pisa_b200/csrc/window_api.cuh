@@ -42,7 +42,7 @@ pisa_status_t check_window(const pisa_window_t& w, pisa::Window* out) {
   if (w.left < -1 || w.right < -1 || w.sinks < 0)
     return fail(PISA_ERR_INVALID_ARG, "window left=%d right=%d (must be >= -1) sinks=%d (must be >= 0)", w.left,
                 w.right, w.sinks);
-  const auto reach = [](int32_t x) { return x < 0 || x > pisa::kMaxTokens ? pisa::kMaxTokens : x; };
+  const auto reach = [](int32_t x) { return x < 0 || x >= pisa::kMaxTokens ? pisa::kMaxTokens - 1 : x; };
   *out = pisa::Window{reach(w.left), reach(w.right), reach(w.sinks)};
   return ok();
 }
@@ -93,12 +93,82 @@ pisa_status_t launch_cache(Kernel k, const pisa::CacheParams& p, int d, int sms,
   return check_launch(what);
 }
 
+// codes of 8 bits [d2][d1][d0], box {d0, box1, 1}, rows contiguous in shared memory
+pisa_status_t make_code_map(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box1) {
+  auto fn = encode_fn();
+  if (!fn) return fail(PISA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[3] = {d0, d1, d2};
+  cuuint64_t strides[2] = {d0, d0 * d1};
+  cuuint32_t box[3] = {uint32_t(d0), box1, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PISA_ERR_CUDA, "cuTensorMapEncodeTiled (codes) failed (%d)", int(r));
+  return ok();
+}
+
+// CTAs along a key head's rows, and the runs that their tiles are cut into so that few rows
+// over a long cache still fill the SMs (at least two tiles a run).
+constexpr int kSms = 148;
+void plan_attend(pisa::AttendTcParams* p, int64_t keys) {
+  const int64_t rows = int64_t(p->Hq / p->Hkv) * p->N;
+  p->pairs = int((rows + 255) / 256);
+  const int64_t ctas = int64_t(p->B) * p->Hkv * p->pairs, tiles = (keys + 127) / 128;
+  int64_t splits = kSms / ctas;
+  if (splits > tiles / 2) splits = tiles / 2;
+  p->splits = int(splits < 1 ? 1 : splits);
+}
+size_t attend_workspace(const pisa::AttendTcParams& p, int d) {
+  return p.splits > 1 ? size_t(p.splits) * p.B * p.Hq * p.N * (size_t(d) + 1) * 4 : 0;
+}
+
 template <int D, int KV>
-pisa_status_t launch_attend(const pisa::AttendParams& p, cudaStream_t st) {
+pisa_status_t launch_attend_tc(pisa::AttendTcParams p, const void* K, const void* V, int page, int num_pages,
+                               void* workspace, cudaStream_t st) {
+  using C = pisa::AttendTcCfg<D, KV>;
+  CUtensorMap mK, mV;
+  if constexpr (KV == pisa::kKvPlain) {
+    PISA_TRY(make_map(&mK, K, D, uint64_t(p.N), uint64_t(p.B) * p.Hkv, 128));
+    PISA_TRY(make_map(&mV, V, D, uint64_t(p.N), uint64_t(p.B) * p.Hkv, 128));
+  } else if constexpr (KV == pisa::kKvPaged) {
+    PISA_TRY(make_map(&mK, K, D, uint64_t(page), uint64_t(num_pages) * p.Hkv, uint32_t(page)));
+    PISA_TRY(make_map(&mV, V, D, uint64_t(page), uint64_t(num_pages) * p.Hkv, uint32_t(page)));
+  } else {
+    PISA_TRY(make_code_map(&mK, K, D, uint64_t(page), uint64_t(num_pages) * p.Hkv, uint32_t(page)));
+    PISA_TRY(make_code_map(&mV, V, D, uint64_t(page), uint64_t(num_pages) * p.Hkv, uint32_t(page)));
+  }
   const int64_t rows = int64_t(p.B) * p.Hq * p.N;
-  const unsigned grid = unsigned((rows + pisa::kRowWarps - 1) / pisa::kRowWarps);
-  pisa::attend_rows_kernel<D, KV><<<grid, 32 * pisa::kRowWarps, 0, st>>>(p);
-  return check_launch("attend_rows_kernel");
+  if (p.splits > 1) {
+    p.part = static_cast<float*>(workspace);
+    p.part_lse = p.part + size_t(p.splits) * rows * D;
+  }
+  auto k = pisa::attend_tc_kernel<D, KV>;
+  PISA_TRY(set_smem(k, C::SMEM));
+  const unsigned grid = unsigned(p.pairs) * unsigned(p.B) * unsigned(p.Hkv) * unsigned(p.splits);
+  k<<<grid, C::kThreads, C::SMEM, st>>>(mK, mV, p);
+  PISA_TRY(check_launch("attend_tc_kernel"));
+  if (p.splits > 1) {
+    pisa::attend_join_kernel<D><<<unsigned((rows + 3) / 4), 128, 0, st>>>(p, KV != pisa::kKvPlain);
+    PISA_TRY(check_launch("attend_join_kernel"));
+  }
+  return ok();
+}
+
+// sizes and plan of a paged call (the longest sequence the table can hold, or the window's reach)
+pisa::AttendTcParams paged_plan(const pisa_cache_t& c, const pisa_sequences_t& s, int32_t Hq, const pisa::Pages& g,
+                                const pisa::Window& w) {
+  pisa::AttendTcParams a{};
+  a.pages = g;
+  a.B = s.B;
+  a.Hq = Hq;
+  a.Hkv = c.Hkv;
+  a.N = s.N;
+  a.win = w;
+  const int64_t cap = int64_t(s.max_pages) * c.page;
+  const int64_t seen = int64_t(w.left) + w.right + s.N + w.sinks;
+  plan_attend(&a, seen < cap ? seen : cap);
+  return a;
 }
 
 template <int D>
@@ -144,7 +214,10 @@ pisa_status_t pisa_window_attention(const void* Q, const void* K, const void* V,
   p.N = shape.N;
   p.scale = scale;
   auto st = static_cast<cudaStream_t>(stream);
-  return shape.d == 128 ? launch_attend<128, pisa::kKvPlain>(p, st) : launch_attend<64, pisa::kKvPlain>(p, st);
+  pisa::AttendTcParams a{p.Q, p.O, lse, nullptr, nullptr, p.pages, p.B, p.Hq, p.Hkv, p.N, 0, 1, p.win, scale};
+  plan_attend(&a, 0);
+  return shape.d == 128 ? launch_attend_tc<128, pisa::kKvPlain>(a, K, V, 0, 0, nullptr, st)
+                        : launch_attend_tc<64, pisa::kKvPlain>(a, K, V, 0, 0, nullptr, st);
 }
 
 pisa_status_t pisa_window_attention_backward_workspace(pisa_window_shape_t shape, pisa_window_t window,
@@ -253,6 +326,8 @@ pisa_status_t pisa_paged_attention_workspace(pisa_cache_t cache, pisa_sequences_
   PISA_TRY(check_cache(cache, seqs, Hq, &empty, &g));
   pisa::Window w;
   PISA_TRY(check_window(window, &w));
+  if (empty) return ok();
+  *bytes = attend_workspace(paged_plan(cache, seqs, Hq, g, w), cache.d);
   return ok();
 }
 
@@ -273,18 +348,16 @@ pisa_status_t pisa_paged_attention(const void* Q, pisa_cache_t cache, pisa_seque
   PISA_TRY(check_workspace(workspace, workspace_bytes, need));
   int sms = 0;
   PISA_TRY(check_device(&sms));
-  p.Q = static_cast<const bf16*>(Q);
-  p.O = static_cast<bf16*>(O);
-  p.lse = lse;
-  p.B = seqs.B;
-  p.Hq = Hq;
-  p.Hkv = cache.Hkv;
-  p.N = seqs.N;
-  p.scale = scale;
+  pisa::AttendTcParams a = paged_plan(cache, seqs, Hq, p.pages, p.win);
+  a.Q = static_cast<const bf16*>(Q);
+  a.O = static_cast<bf16*>(O);
+  a.lse = lse;
+  a.scale = scale;
   auto st = static_cast<cudaStream_t>(stream);
+  const auto run = [&](auto k) { return k(a, cache.K, cache.V, cache.page, cache.num_pages, workspace, st); };
   if (cache.type == PISA_CACHE_E4M3)
-    return cache.d == 128 ? launch_attend<128, pisa::kKvPagedE4m3>(p, st) : launch_attend<64, pisa::kKvPagedE4m3>(p, st);
-  return cache.d == 128 ? launch_attend<128, pisa::kKvPaged>(p, st) : launch_attend<64, pisa::kKvPaged>(p, st);
+    return cache.d == 128 ? run(launch_attend_tc<128, pisa::kKvPagedE4m3>) : run(launch_attend_tc<64, pisa::kKvPagedE4m3>);
+  return cache.d == 128 ? run(launch_attend_tc<128, pisa::kKvPaged>) : run(launch_attend_tc<64, pisa::kKvPaged>);
 }
 
 }  // extern "C"
