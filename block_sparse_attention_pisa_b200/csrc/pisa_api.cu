@@ -19,8 +19,8 @@
 #include "stats_tc.cuh"
 #include "host_pipeline.cuh"
 #include "cache.cuh"
-#include "window_attention.cuh"
 #include "attend_tc.cuh"
+#include "attend_grad_tc.cuh"
 
 using pisa::bf16;
 

@@ -171,17 +171,55 @@ pisa::AttendTcParams paged_plan(const pisa_cache_t& c, const pisa_sequences_t& s
   return a;
 }
 
+// How the key tiles of the gradient are cut into runs of query tiles: about two CTAs per SM if
+// all were equal, so that a tile which every row sees (the first tokens) is cut and the
+// window's are not.
+struct GradPlan {
+  int run, runs, slots;
+  size_t delta_bytes, bytes;
+};
+GradPlan plan_grad(const pisa_window_shape_t& s, const pisa::Window& w) {
+  const int kts = (s.N + 127) / 128, G = s.Hq / s.Hkv;
+  const int64_t heads = int64_t(s.B) * s.Hkv;
+  int64_t total = 0;
+  for (int kt = 0; kt < kts; ++kt) total += int64_t(G) * pisa::QueryRange(w, kt, s.N).count;
+  const int64_t run = (total * heads + 2 * kSms - 1) / (2 * kSms);
+  GradPlan g{};
+  g.run = int(run < 16 ? 16 : (run > INT32_MAX ? INT32_MAX : run));
+  for (int kt = 0; kt < kts; ++kt) {
+    const int r = pisa::query_runs(G * pisa::QueryRange(w, kt, s.N).count, g.run);
+    g.runs += r;
+    if (r > 1) g.slots += r;
+  }
+  g.delta_bytes = (size_t(s.B) * s.Hq * s.N * 4 + 255) / 256 * 256;
+  g.bytes = g.delta_bytes + size_t(heads) * g.slots * 2 * 128 * s.d * 4;
+  return g;
+}
+
 template <int D>
-pisa_status_t launch_attend_backward(const pisa::AttendParams& p, cudaStream_t st) {
-  const int64_t rows = int64_t(p.B) * p.Hq * p.N, keys = int64_t(p.B) * p.Hkv * p.N;
-  const unsigned gq = unsigned((rows + pisa::kRowWarps - 1) / pisa::kRowWarps);
-  const unsigned gk = unsigned((keys + pisa::kRowWarps - 1) / pisa::kRowWarps);
-  pisa::attend_delta_kernel<D><<<gq, 32 * pisa::kRowWarps, 0, st>>>(p);
-  PISA_TRY(check_launch("attend_delta_kernel"));
-  pisa::attend_dq_kernel<D><<<gq, 32 * pisa::kRowWarps, 0, st>>>(p);
+pisa_status_t launch_grad(pisa::AttendGradParams p, const GradPlan& g, const void* K, const void* V, cudaStream_t st) {
+  const uint64_t heads = uint64_t(p.B) * p.Hkv, N = uint64_t(p.N);
+  CUtensorMap mK, mV, mQ, mG;
+  PISA_TRY(make_map(&mK, K, D, N, heads, 128));
+  PISA_TRY(make_map(&mV, V, D, N, heads, 128));
+  PISA_TRY(make_map(&mQ, p.Q, D, N, uint64_t(p.B) * p.Hq, 64));
+  PISA_TRY(make_map(&mG, p.dO, D, N, uint64_t(p.B) * p.Hq, 64));
+  auto kq = pisa::attend_dq_kernel<D>;
+  auto kk = pisa::attend_dkv_kernel<D>;
+  using Cq = pisa::AttendDqCfg<D>;
+  using Ck = pisa::AttendDkvCfg<D>;
+  PISA_TRY(set_smem(kq, Cq::SMEM));
+  PISA_TRY(set_smem(kk, Ck::SMEM));
+  const unsigned row_tiles = unsigned((int64_t(p.Hq / p.Hkv) * p.N + 127) / 128);
+  kq<<<row_tiles * unsigned(heads), Cq::kThreads, Cq::SMEM, st>>>(mK, mV, p);
   PISA_TRY(check_launch("attend_dq_kernel"));
-  pisa::attend_dkv_kernel<D><<<gk, 32 * pisa::kRowWarps, 0, st>>>(p);
-  return check_launch("attend_dkv_kernel");
+  kk<<<unsigned(g.runs) * unsigned(heads), Ck::kThreads, Ck::SMEM, st>>>(mK, mV, mQ, mG, p);
+  PISA_TRY(check_launch("attend_dkv_kernel"));
+  if (g.slots > 0) {
+    pisa::attend_dkv_join_kernel<D><<<unsigned((N + 127) / 128 * heads), 256, 0, st>>>(p);
+    PISA_TRY(check_launch("attend_dkv_join_kernel"));
+  }
+  return ok();
 }
 
 }  // namespace
@@ -192,8 +230,8 @@ pisa_status_t pisa_window_attention(const void* Q, const void* K, const void* V,
                                     pisa_window_t window, float scale, void* O, float* lse, void* stream) {
   bool empty = false;
   PISA_TRY(check_heads(shape.B, shape.Hq, shape.Hkv, shape.N, shape.d, &empty));
-  pisa::AttendParams p{};
-  PISA_TRY(check_window(window, &p.win));
+  pisa::AttendTcParams a{};
+  PISA_TRY(check_window(window, &a.win));
   PISA_TRY(check_scale(scale));
   if (empty) return ok();
   PISA_TRY(check_ptr(Q, "Q"));
@@ -203,19 +241,16 @@ pisa_status_t pisa_window_attention(const void* Q, const void* K, const void* V,
   if (lse != nullptr) PISA_TRY(check_aligned(lse, "lse", 4));
   int sms = 0;
   PISA_TRY(check_device(&sms));
-  p.Q = static_cast<const bf16*>(Q);
-  p.K = static_cast<const bf16*>(K);
-  p.V = static_cast<const bf16*>(V);
-  p.O = static_cast<bf16*>(O);
-  p.lse = lse;
-  p.B = shape.B;
-  p.Hq = shape.Hq;
-  p.Hkv = shape.Hkv;
-  p.N = shape.N;
-  p.scale = scale;
-  auto st = static_cast<cudaStream_t>(stream);
-  pisa::AttendTcParams a{p.Q, p.O, lse, nullptr, nullptr, p.pages, p.B, p.Hq, p.Hkv, p.N, 0, 1, p.win, scale};
+  a.Q = static_cast<const bf16*>(Q);
+  a.O = static_cast<bf16*>(O);
+  a.lse = lse;
+  a.B = shape.B;
+  a.Hq = shape.Hq;
+  a.Hkv = shape.Hkv;
+  a.N = shape.N;
+  a.scale = scale;
   plan_attend(&a, 0);
+  auto st = static_cast<cudaStream_t>(stream);
   return shape.d == 128 ? launch_attend_tc<128, pisa::kKvPlain>(a, K, V, 0, 0, nullptr, st)
                         : launch_attend_tc<64, pisa::kKvPlain>(a, K, V, 0, 0, nullptr, st);
 }
@@ -229,7 +264,7 @@ pisa_status_t pisa_window_attention_backward_workspace(pisa_window_shape_t shape
   pisa::Window w;
   PISA_TRY(check_window(window, &w));
   if (empty) return ok();
-  *bytes = size_t(shape.B) * shape.Hq * shape.N * 4;  // delta
+  *bytes = plan_grad(shape, w).bytes;
   return ok();
 }
 
@@ -241,7 +276,7 @@ pisa_status_t pisa_window_attention_backward(const void* dO, const void* Q, cons
   PISA_TRY(pisa_window_attention_backward_workspace(shape, window, &need));
   PISA_TRY(check_scale(scale));
   if (need == 0) return ok();  // empty problem: nothing touched
-  pisa::AttendParams p{};
+  pisa::AttendGradParams p{};
   PISA_TRY(check_window(window, &p.win));
   const void* bufs[8] = {dO, Q, K, V, O, dQ, dK, dV};
   const char* names[8] = {"dO", "Q", "K", "V", "O", "dQ", "dK", "dV"};
@@ -251,10 +286,8 @@ pisa_status_t pisa_window_attention_backward(const void* dO, const void* Q, cons
   int sms = 0;
   PISA_TRY(check_device(&sms));
   p.Q = static_cast<const bf16*>(Q);
-  p.K = static_cast<const bf16*>(K);
-  p.V = static_cast<const bf16*>(V);
-  p.O = const_cast<bf16*>(static_cast<const bf16*>(O));
-  p.lse = const_cast<float*>(lse);
+  p.O = static_cast<const bf16*>(O);
+  p.lse = lse;
   p.dO = static_cast<const bf16*>(dO);
   p.dQ = static_cast<bf16*>(dQ);
   p.dK = static_cast<bf16*>(dK);
@@ -265,8 +298,13 @@ pisa_status_t pisa_window_attention_backward(const void* dO, const void* Q, cons
   p.Hkv = shape.Hkv;
   p.N = shape.N;
   p.scale = scale;
+  const GradPlan g = plan_grad(shape, p.win);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + g.delta_bytes);
+  p.run = g.run;
+  p.runs = g.runs;
+  p.slots = g.slots;
   auto st = static_cast<cudaStream_t>(stream);
-  return shape.d == 128 ? launch_attend_backward<128>(p, st) : launch_attend_backward<64>(p, st);
+  return shape.d == 128 ? launch_grad<128>(p, g, K, V, st) : launch_grad<64>(p, g, K, V, st);
 }
 
 pisa_status_t pisa_cache_write(const void* K, const void* V, pisa_cache_t cache, pisa_sequences_t seqs,
@@ -335,9 +373,10 @@ pisa_status_t pisa_paged_attention(const void* Q, pisa_cache_t cache, pisa_seque
                                    pisa_window_t window, float scale, void* O, float* lse, void* workspace,
                                    size_t workspace_bytes, void* stream) {
   bool empty = false;
-  pisa::AttendParams p{};
-  PISA_TRY(check_cache(cache, seqs, Hq, &empty, &p.pages));
-  PISA_TRY(check_window(window, &p.win));
+  pisa::Pages g{};
+  pisa::Window w;
+  PISA_TRY(check_cache(cache, seqs, Hq, &empty, &g));
+  PISA_TRY(check_window(window, &w));
   PISA_TRY(check_scale(scale));
   if (empty) return ok();
   PISA_TRY(check_ptr(Q, "Q"));
@@ -348,7 +387,7 @@ pisa_status_t pisa_paged_attention(const void* Q, pisa_cache_t cache, pisa_seque
   PISA_TRY(check_workspace(workspace, workspace_bytes, need));
   int sms = 0;
   PISA_TRY(check_device(&sms));
-  pisa::AttendTcParams a = paged_plan(cache, seqs, Hq, p.pages, p.win);
+  pisa::AttendTcParams a = paged_plan(cache, seqs, Hq, g, w);
   a.Q = static_cast<const bf16*>(Q);
   a.O = static_cast<bf16*>(O);
   a.lse = lse;
