@@ -21,6 +21,7 @@
 #include "cache.cuh"
 #include "attend_tc.cuh"
 #include "attend_grad_tc.cuh"
+#include "attend_token.cuh"
 
 using pisa::bf16;
 

@@ -157,7 +157,7 @@ pisa_status_t launch_attend_tc(pisa::AttendTcParams p, const void* K, const void
 
 // sizes and plan of a paged call (the longest sequence the table can hold, or the window's reach)
 pisa::AttendTcParams paged_plan(const pisa_cache_t& c, const pisa_sequences_t& s, int32_t Hq, const pisa::Pages& g,
-                                const pisa::Window& w) {
+                                const pisa::Window& w, int64_t* keys) {
   pisa::AttendTcParams a{};
   a.pages = g;
   a.B = s.B;
@@ -167,8 +167,41 @@ pisa::AttendTcParams paged_plan(const pisa_cache_t& c, const pisa_sequences_t& s
   a.win = w;
   const int64_t cap = int64_t(s.max_pages) * c.page;
   const int64_t seen = int64_t(w.left) + w.right + s.N + w.sinks;
-  plan_attend(&a, seen < cap ? seen : cap);
+  *keys = seen < cap ? seen : cap;
+  plan_attend(&a, *keys);
   return a;
+}
+
+// Up to 16 rows per key head: the token kernel. Two CTAs per SM, fewer if the cache cannot
+// hold as many chunks.
+bool few_rows(const pisa::AttendTcParams& a) { return int64_t(a.Hq / a.Hkv) * a.N <= pisa::kTokenRows; }
+int token_ctas(const pisa::AttendTcParams& a, int64_t keys, int chunk) {
+  const int64_t most = int64_t(a.B) * a.Hkv * ((keys + chunk - 1) / chunk + 1);
+  return int(most < 2 * kSms ? most : 2 * kSms);
+}
+int token_chunk(int d, int type) { return pisa::kTokenWarps * 4096 / (type == PISA_CACHE_E4M3 ? d : 2 * d); }
+size_t token_workspace(int ctas, int d) { return size_t(2) * ctas * pisa::kTokenRows * (size_t(d) + 1) * 4; }
+
+template <int D, bool E4M3>
+pisa_status_t launch_token(const pisa::AttendTcParams& a, int ctas, void* workspace, cudaStream_t st) {
+  pisa::AttendTokenParams p{a.Q, a.O, a.lse, static_cast<float*>(workspace), nullptr, a.pages, a.B, a.Hq, a.Hkv, a.N,
+                            ctas, a.win, a.scale};
+  p.part_lse = p.part + size_t(2) * ctas * pisa::kTokenRows * D;
+  pisa::attend_token_kernel<D, E4M3><<<unsigned(ctas), 32 * pisa::kTokenWarps, 0, st>>>(p);
+  PISA_TRY(check_launch("attend_token_kernel"));
+  // the join's blocks start while the pieces are still being computed, and wait for them
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(a.B) * unsigned(a.Hkv));
+  cfg.blockDim = dim3(32 * pisa::kTokenWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, pisa::attend_token_join_kernel<D, E4M3>, p);
+  if (e != cudaSuccess) return fail(PISA_ERR_CUDA, "attend_token_join_kernel launch: %s", cudaGetErrorString(e));
+  return check_launch("attend_token_join_kernel");
 }
 
 // How the key tiles of the gradient are cut into runs of query tiles: about two CTAs per SM if
@@ -365,7 +398,10 @@ pisa_status_t pisa_paged_attention_workspace(pisa_cache_t cache, pisa_sequences_
   pisa::Window w;
   PISA_TRY(check_window(window, &w));
   if (empty) return ok();
-  *bytes = attend_workspace(paged_plan(cache, seqs, Hq, g, w), cache.d);
+  int64_t keys = 0;
+  const pisa::AttendTcParams a = paged_plan(cache, seqs, Hq, g, w, &keys);
+  *bytes = few_rows(a) ? token_workspace(token_ctas(a, keys, token_chunk(cache.d, cache.type)), cache.d)
+                       : attend_workspace(a, cache.d);
   return ok();
 }
 
@@ -387,14 +423,22 @@ pisa_status_t pisa_paged_attention(const void* Q, pisa_cache_t cache, pisa_seque
   PISA_TRY(check_workspace(workspace, workspace_bytes, need));
   int sms = 0;
   PISA_TRY(check_device(&sms));
-  pisa::AttendTcParams a = paged_plan(cache, seqs, Hq, g, w);
+  int64_t keys = 0;
+  pisa::AttendTcParams a = paged_plan(cache, seqs, Hq, g, w, &keys);
   a.Q = static_cast<const bf16*>(Q);
   a.O = static_cast<bf16*>(O);
   a.lse = lse;
   a.scale = scale;
   auto st = static_cast<cudaStream_t>(stream);
+  const bool codes = cache.type == PISA_CACHE_E4M3;
+  if (few_rows(a)) {
+    const int ctas = token_ctas(a, keys, token_chunk(cache.d, cache.type));
+    if (codes)
+      return cache.d == 128 ? launch_token<128, true>(a, ctas, workspace, st) : launch_token<64, true>(a, ctas, workspace, st);
+    return cache.d == 128 ? launch_token<128, false>(a, ctas, workspace, st) : launch_token<64, false>(a, ctas, workspace, st);
+  }
   const auto run = [&](auto k) { return k(a, cache.K, cache.V, cache.page, cache.num_pages, workspace, st); };
-  if (cache.type == PISA_CACHE_E4M3)
+  if (codes)
     return cache.d == 128 ? run(launch_attend_tc<128, pisa::kKvPagedE4m3>) : run(launch_attend_tc<64, pisa::kKvPagedE4m3>);
   return cache.d == 128 ? run(launch_attend_tc<128, pisa::kKvPaged>) : run(launch_attend_tc<64, pisa::kKvPaged>);
 }
