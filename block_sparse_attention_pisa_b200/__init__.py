@@ -449,43 +449,68 @@ def pisa_host_static(Q, K, V, block: int, topk: int, order: int = 1, scale: floa
     return out
 
 
-def _heads(Q, K):
-    """(B, Hq, Hkv, N, d) of grouped-head operands [B, Hq, N, d] and [B, Hkv, N, d]."""
-    for t, name in ((Q, "Q"), (K, "K")):
-        if t.dim() != 4:
-            raise ValueError(f"{name} must be a [B, H, N, d] tensor")
-    B, Hq, N, d = Q.shape
-    return B, Hq, K.shape[1], N, d
+def _check_operands(checks):
+    """The operands' CUDA device, if every (tensor, name, shape, dtype) entry is a contiguous
+    tensor of its shape and dtype on it. Plain tensors that fit pass in one comparison each;
+    anything else takes the checks that name what is wrong, shapes and dtypes before devices."""
+    import torch
+    dev = getattr(checks[0][0], "device", None)
+    for t, _, shp, dt in checks:
+        if not (type(t) is torch.Tensor and t.shape == shp and t.dtype is dt and t.device == dev and t.is_contiguous()):
+            break
+    else:
+        if dev.type == "cuda":
+            return dev
+    for t, name, shp, dt in checks:
+        _require(t, name, shp, dt)
+    dev = _device_of(checks[0][0])
+    for t, name, _, _ in checks:
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return dev
+
+
+def _launch(fn, dev, *args):
+    """fn(*args, stream) on ``dev`` (made current for the call if it is not) and its current stream."""
+    import torch
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
+
+
+def _heads(t, name: str):
+    """The shape of a [B, H, N, d] operand."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError(f"{name} must be a [B, H, N, d] tensor")
+    return t.shape
 
 
 def _window(left: int, right: int, sinks: int) -> Window:
     for x, name in ((left, "left"), (right, "right"), (sinks, "sinks")):
-        if not -2 ** 31 <= int(x) < 2 ** 31:
+        if not -2 ** 31 <= x < 2 ** 31:
             raise ValueError(f"{name}={x} does not fit 32 bits")
-    return Window(int(left), int(right), int(sinks))
-
-
-def _require_all(checks, dev):
-    """``_require`` for (tensor, name, shape, dtype) entries; shapes and dtypes first, then the device."""
-    for t, name, shp, dt in checks:
-        _require(t, name, shp, dt)
-    for t, name, _, _ in checks:
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return Window(left, right, sinks)
 
 
 def _workspace(t, nbytes: int, dev):
-    """The caller's workspace tensor (uint8, checked) or a new one."""
+    """(address, bytes, tensor) of the caller's workspace tensor (uint8, checked) or a new one;
+    the tensor has to live until the call is enqueued."""
     import torch
     if t is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        if nbytes == 0:
+            return None, 0, None
+        t = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return t.data_ptr(), nbytes, t
     if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     if t.numel() < nbytes:
         raise ValueError(f"workspace holds {t.numel()} bytes, {nbytes} are needed")
     if t.device != dev:
         raise ValueError(f"workspace is on {t.device}, expected {dev}")
-    return t
+    return t.data_ptr(), t.numel(), t
 
 
 def window_attention(Q, K, V, left: int = -1, right: int = -1, sinks: int = 0, scale: float | None = None, out=None,
@@ -495,23 +520,18 @@ def window_attention(Q, K, V, left: int = -1, right: int = -1, sinks: int = 0, s
     K, V: bf16 [B, Hkv, N, d], query head h reading key head ``h // (Hq // Hkv)``. Returns
     (O bf16 [B, Hq, N, d], lse fp32 [B, Hq, N], the natural logarithm of each row's sum)."""
     import torch
-    B, Hq, Hkv, N, d = _heads(Q, K)
-    checks = [(Q, "Q", (B, Hq, N, d), torch.bfloat16), (K, "K", (B, Hkv, N, d), torch.bfloat16),
-              (V, "V", (B, Hkv, N, d), torch.bfloat16)]
+    B, Hq, N, d = q = _heads(Q, "Q")
+    kv, stat = (B, _heads(K, "K")[1], N, d), (B, Hq, N)
+    checks = [(Q, "Q", q, torch.bfloat16), (K, "K", kv, torch.bfloat16), (V, "V", kv, torch.bfloat16)]
     if out is not None:
-        checks.append((out, "O", (B, Hq, N, d), torch.bfloat16))
+        checks.append((out, "O", q, torch.bfloat16))
     if lse is not None:
-        checks.append((lse, "lse", (B, Hq, N), torch.float32))
-    for t, name, shp, dt in checks:
-        _require(t, name, shp, dt)
-    dev = _device_of(Q)
-    _require_all(checks, dev)
-    scale = d ** -0.5 if scale is None else scale
+        checks.append((lse, "lse", stat, torch.float32))
+    dev = _check_operands(checks)
     O = torch.empty_like(Q) if out is None else out
-    lse = torch.empty((B, Hq, N), device=dev, dtype=torch.float32) if lse is None else lse
-    with torch.cuda.device(dev):
-        _check(lib().pisa_window_attention(_ptr(Q), _ptr(K), _ptr(V), WindowShape(B, Hq, Hkv, N, d),
-                                           _window(left, right, sinks), float(scale), _ptr(O), _ptr(lse), _stream(Q)))
+    lse = Q.new_empty(stat, dtype=torch.float32) if lse is None else lse
+    _launch(lib().pisa_window_attention, dev, Q.data_ptr(), K.data_ptr(), V.data_ptr(), WindowShape(B, Hq, kv[1], N, d),
+            _window(left, right, sinks), d ** -0.5 if scale is None else float(scale), O.data_ptr(), lse.data_ptr())
     return O, lse
 
 
@@ -521,7 +541,7 @@ def window_attention_backward_workspace(B: int, Hq: int, Hkv: int, N: int, d: in
     n = ctypes.c_size_t(0)
     _check(lib().pisa_window_attention_backward_workspace(WindowShape(B, Hq, Hkv, N, d), _window(left, right, sinks),
                                                           ctypes.byref(n)))
-    return int(n.value)
+    return n.value
 
 
 def window_attention_backward(dO, Q, K, V, O, lse, left: int = -1, right: int = -1, sinks: int = 0,
@@ -531,24 +551,21 @@ def window_attention_backward(dO, Q, K, V, O, lse, left: int = -1, right: int = 
     preallocated; ``workspace``: a uint8 tensor of at least
     ``window_attention_backward_workspace`` bytes that no other call uses meanwhile."""
     import torch
-    B, Hq, Hkv, N, d = _heads(Q, K)
-    q, kv = (B, Hq, N, d), (B, Hkv, N, d)
-    checks = [(dO, "dO", q, torch.bfloat16), (Q, "Q", q, torch.bfloat16), (K, "K", kv, torch.bfloat16),
-              (V, "V", kv, torch.bfloat16), (O, "O", q, torch.bfloat16), (lse, "lse", (B, Hq, N), torch.float32)]
+    B, Hq, N, d = q = _heads(Q, "Q")
+    Hkv = _heads(K, "K")[1]
+    kv, bf = (B, Hkv, N, d), torch.bfloat16
+    checks = [(dO, "dO", q, bf), (Q, "Q", q, bf), (K, "K", kv, bf), (V, "V", kv, bf), (O, "O", q, bf),
+              (lse, "lse", (B, Hq, N), torch.float32)]
     if out is not None:
-        checks += [(t, name, s, torch.bfloat16) for t, name, s in zip(out, ("dQ", "dK", "dV"), (q, kv, kv))]
-    for t, name, shp, dt in checks:
-        _require(t, name, shp, dt)
-    dev = _device_of(Q)
-    _require_all(checks, dev)
-    scale = d ** -0.5 if scale is None else scale
-    nbytes = window_attention_backward_workspace(B, Hq, Hkv, N, d, left, right, sinks)
-    ws = _workspace(workspace, nbytes, dev)
-    dQ, dK, dV = (torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V)) if out is None else out
-    with torch.cuda.device(dev):
-        _check(lib().pisa_window_attention_backward(
-            _ptr(dO), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse), WindowShape(B, Hq, Hkv, N, d),
-            _window(left, right, sinks), float(scale), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(ws), ws.numel(), _stream(Q)))
+        dQ, dK, dV = out
+        checks += [(dQ, "dQ", q, bf), (dK, "dK", kv, bf), (dV, "dV", kv, bf)]
+    dev = _check_operands(checks)
+    ws, nbytes, hold = _workspace(workspace, window_attention_backward_workspace(B, Hq, Hkv, N, d, left, right, sinks), dev)
+    if out is None:
+        dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V)
+    _launch(lib().pisa_window_attention_backward, dev, dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
+            lse.data_ptr(), WindowShape(B, Hq, Hkv, N, d), _window(left, right, sinks), d ** -0.5 if scale is None else float(scale),
+            dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws, nbytes)
     return dQ, dK, dV
 
 
@@ -574,8 +591,8 @@ def paged_cache(num_pages: int, Hkv: int, page: int, d: int, dtype=None, device=
     return PagedCache(K, V, *(torch.zeros((num_pages, Hkv, page), dtype=torch.float32, device=device) for _ in "KV"))
 
 
-def _cache_args(cache, page_table, kv_lens, q_lens, B: int, N: int, dev):
-    """(pisa_cache_t, pisa_sequences_t) of checked tensors on ``dev``."""
+def _cache_checks(cache, page_table, kv_lens, q_lens, B: int):
+    """``_check_operands`` entries of a cache and its sequences."""
     import torch
     K = cache.K
     if not isinstance(K, torch.Tensor) or K.dim() != 4:
@@ -584,21 +601,26 @@ def _cache_args(cache, page_table, kv_lens, q_lens, B: int, N: int, dev):
         raise ValueError(f"cache K has dtype {K.dtype}, expected bfloat16 or float8_e4m3fn")
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be an int32 [B, max_pages] tensor")
-    max_pages = page_table.shape[1]
-    checks = [(K, "cache K", K.shape, K.dtype), (cache.V, "cache V", K.shape, K.dtype),
-              (page_table, "page_table", (B, max_pages), torch.int32), (kv_lens, "kv_lens", (B,), torch.int32)]
-    quantised = K.dtype != torch.bfloat16
-    if quantised:
-        checks += [(cache.k_scale, "k_scale", K.shape[:3], torch.float32),
-                   (cache.v_scale, "v_scale", K.shape[:3], torch.float32)]
+    shape, i32 = K.shape, torch.int32
+    checks = [(K, "cache K", shape, K.dtype), (cache.V, "cache V", shape, K.dtype),
+              (page_table, "page_table", (B, page_table.shape[1]), i32), (kv_lens, "kv_lens", (B,), i32)]
+    if K.dtype != torch.bfloat16:
+        checks += [(cache.k_scale, "k_scale", shape[:3], torch.float32), (cache.v_scale, "v_scale", shape[:3], torch.float32)]
     if q_lens is not None:
-        checks.append((q_lens, "q_lens", (B,), torch.int32))
-    _require_all(checks, dev)
-    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    num_pages, Hkv, page, d = K.shape
-    scales = (at(cache.k_scale), at(cache.v_scale)) if quantised else (None, None)
-    return (CacheArgs(at(K), at(cache.V), *scales, num_pages, Hkv, page, d, int(quantised)),
-            Sequences(at(page_table), at(kv_lens), at(q_lens), B, N, max_pages))
+        checks.append((q_lens, "q_lens", (B,), i32))
+    return checks
+
+
+def _cache_args(cache, page_table, kv_lens, q_lens, B: int, N: int):
+    """(pisa_cache_t, pisa_sequences_t) of checked tensors."""
+    import torch
+    K, V, ks, vs = cache
+    if K.dtype == torch.bfloat16:
+        c = CacheArgs(K.data_ptr(), V.data_ptr(), None, None, *K.shape, 0)
+    else:
+        c = CacheArgs(K.data_ptr(), V.data_ptr(), ks.data_ptr(), vs.data_ptr(), *K.shape, 1)
+    return c, Sequences(page_table.data_ptr(), kv_lens.data_ptr(), None if q_lens is None else q_lens.data_ptr(), B, N,
+                        page_table.shape[1])
 
 
 def cache_write(K, V, cache, page_table, kv_lens, q_lens=None):
@@ -607,48 +629,44 @@ def cache_write(K, V, cache, page_table, kv_lens, q_lens=None):
     ``kv_lens[b] - q_lens[b] + t`` (``kv_lens`` counts the new tokens; ``q_lens`` defaults to
     N each), in page ``page_table[b, position // page]``."""
     import torch
-    if K.dim() != 4:
-        raise ValueError("K must be a [B, Hkv, N, d] tensor")
-    B, Hkv, N, d = K.shape
-    for t, name in ((K, "K"), (V, "V")):
-        _require(t, name, K.shape, torch.bfloat16)
-    dev = _device_of(K)
-    if V.device != dev:
-        raise ValueError(f"V is on {V.device}, expected {dev}")
-    c, s = _cache_args(cache, page_table, kv_lens, q_lens, B, N, dev)
-    if (c.Hkv, c.d) != (Hkv, d):
+    B, Hkv, N, d = shape = _heads(K, "K")
+    checks = [(K, "K", shape, torch.bfloat16), (V, "V", shape, torch.bfloat16)]
+    dev = _check_operands(checks + _cache_checks(cache, page_table, kv_lens, q_lens, B))
+    c, s = _cache_args(cache, page_table, kv_lens, q_lens, B, N)
+    if c.Hkv != Hkv or c.d != d:
         raise ValueError(f"the cache holds {c.Hkv} heads of {c.d}, K has {Hkv} of {d}")
-    with torch.cuda.device(dev):
-        _check(lib().pisa_cache_write(_ptr(K), _ptr(V), c, s, _stream(K)))
+    _launch(lib().pisa_cache_write, dev, K.data_ptr(), V.data_ptr(), c, s)
 
 
 def cache_read(cache, page_table, kv_lens, N: int, out=None):
     """(K, V) bf16 [B, Hkv, N, d]: the first N tokens of every sequence. Rows behind a
     sequence's last are left as they are in ``out`` = (K, V), zero without it."""
     import torch
-    dev = _device_of(cache.K)
-    B = page_table.shape[0]
-    c, s = _cache_args(cache, page_table, kv_lens, None, B, N, dev)
-    shape = (B, c.Hkv, N, c.d)
+    B = len(page_table)
+    checks = _cache_checks(cache, page_table, kv_lens, None, B)
+    shape = (B, cache.K.shape[1], N, cache.K.shape[3])
+    if out is not None:
+        K, V = out
+        checks += [(K, "K", shape, torch.bfloat16), (V, "V", shape, torch.bfloat16)]
+    dev = _check_operands(checks)
     if out is None:
-        out = tuple(torch.zeros(shape, dtype=torch.bfloat16, device=dev) for _ in "KV")
-    K, V = out
-    _require_all([(K, "K", shape, torch.bfloat16), (V, "V", shape, torch.bfloat16)], dev)
-    with torch.cuda.device(dev):
-        _check(lib().pisa_cache_read(c, s, _ptr(K), _ptr(V), _stream(K)))
+        K, V = (torch.zeros(shape, dtype=torch.bfloat16, device=dev) for _ in "KV")
+    c, s = _cache_args(cache, page_table, kv_lens, None, B, N)
+    _launch(lib().pisa_cache_read, dev, c, s, K.data_ptr(), V.data_ptr())
     return K, V
 
 
 def _paged_workspace(c, s, Hq: int, w) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().pisa_paged_attention_workspace(c, s, Hq, w, ctypes.byref(n)))
-    return int(n.value)
+    return n.value
 
 
 def paged_attention_workspace(Q, cache, page_table, kv_lens, left: int = -1, right: int = 0, sinks: int = 0) -> int:
     """Device workspace (bytes) that ``paged_attention`` needs for these operands."""
-    c, s = _cache_args(cache, page_table, kv_lens, None, Q.shape[0], Q.shape[2], Q.device)
-    return _paged_workspace(c, s, Q.shape[1], _window(left, right, sinks))
+    B, Hq, N, _ = _heads(Q, "Q")
+    _check_operands(_cache_checks(cache, page_table, kv_lens, None, B))
+    return _paged_workspace(*_cache_args(cache, page_table, kv_lens, None, B, N), Hq, _window(left, right, sinks))
 
 
 def paged_attention(Q, cache, page_table, kv_lens, q_lens=None, left: int = -1, right: int = 0, sinks: int = 0,
@@ -660,31 +678,26 @@ def paged_attention(Q, cache, page_table, kv_lens, q_lens=None, left: int = -1, 
     left as they are in ``out`` and ``lse``, zero without them. ``workspace``: a uint8 tensor
     of at least ``paged_attention_workspace`` bytes that no other call uses meanwhile."""
     import torch
-    if Q.dim() != 4:
-        raise ValueError("Q must be a [B, Hq, N, d] tensor")
-    B, Hq, N, d = Q.shape
-    checks = [(Q, "Q", (B, Hq, N, d), torch.bfloat16)]
+    B, Hq, N, d = shape = _heads(Q, "Q")
+    stat = (B, Hq, N)
+    checks = [(Q, "Q", shape, torch.bfloat16)]
     if out is not None:
-        checks.append((out, "O", (B, Hq, N, d), torch.bfloat16))
+        checks.append((out, "O", shape, torch.bfloat16))
     if lse is not None:
-        checks.append((lse, "lse", (B, Hq, N), torch.float32))
-    for t, name, shp, dt in checks:
-        _require(t, name, shp, dt)
-    dev = _device_of(Q)
-    _require_all(checks, dev)
-    c, s = _cache_args(cache, page_table, kv_lens, q_lens, B, N, dev)
+        checks.append((lse, "lse", stat, torch.float32))
+    dev = _check_operands(checks + _cache_checks(cache, page_table, kv_lens, q_lens, B))
+    c, s = _cache_args(cache, page_table, kv_lens, q_lens, B, N)
     if c.d != d:
         raise ValueError(f"the cache holds heads of {c.d}, Q has {d}")
     w = _window(left, right, sinks)
-    scale = d ** -0.5 if scale is None else scale
-    ws = _workspace(workspace, _paged_workspace(c, s, Hq, w), dev)
-    new = torch.empty if q_lens is None else torch.zeros
-    O = new(Q.shape, dtype=Q.dtype, device=dev) if out is None else out
-    lse = new((B, Hq, N), dtype=torch.float32, device=dev) if lse is None else lse
-    with torch.cuda.device(dev):
-        _check(lib().pisa_paged_attention(_ptr(Q), c, s, Hq, w, float(scale), _ptr(O), _ptr(lse), _ptr(ws),
-                                          ws.numel(), _stream(Q)))
-    return O, lse
+    ws, nbytes, hold = _workspace(workspace, _paged_workspace(c, s, Hq, w), dev)
+    if out is None:
+        out = torch.empty_like(Q) if q_lens is None else torch.zeros_like(Q)
+    if lse is None:
+        lse = Q.new_empty(stat, dtype=torch.float32) if q_lens is None else Q.new_zeros(stat, dtype=torch.float32)
+    _launch(lib().pisa_paged_attention, dev, Q.data_ptr(), c, s, Hq, w, d ** -0.5 if scale is None else float(scale),
+            out.data_ptr(), lse.data_ptr(), ws, nbytes)
+    return out, lse
 
 
 def device_error(stream_tensor=None):

@@ -1,15 +1,14 @@
 // Paged key/value cache: rows are quantised as they are written, and read back.
 //
 // A row is one token of one key head (d values). In 8 bits it is held as e4m3 codes with one
-// fp32 scale: scale = max(amax|x| / 448, 2^-126), code = e4m3(x / scale) (IEEE division, round
-// to nearest even, so the codes are those of the formula), and read back as
-// bf16(code * scale). The bits of |x| grow with |x| and a NaN's lie above infinity's, so the
-// maximum is taken over the bits: a row with a NaN or an infinity gets the scale NaN, and the
-// whole row reads back as NaN.
+// fp32 scale: scale = max(amax|x| / 448, 2^-126), code = e4m3(x / scale) (the fp32 quotient,
+// rounded to nearest even), and read back as bf16(code * scale). The bits of |x| grow with
+// |x| and a NaN's lie above infinity's, so the maximum is taken over the bits: a row with an
+// infinity or a NaN gets the scale NaN, and the whole row reads back as NaN.
 //
-// Both kernels are bound by memory: each row of x is read once and its codes written once
-// (or the reverse), 16 bytes of x per thread and row, a row per D/8 neighbouring threads; the
-// lengths, the page table and the scales are small beside that.
+// Both kernels are bound by memory: each row of x is read once and its codes written once (or
+// the reverse). A thread takes 16 bytes of the cache's row (16 codes or 8 bf16) of K and of V,
+// kCacheRows rows in flight.
 #pragma once
 
 #include "window.cuh"
@@ -17,7 +16,7 @@
 namespace pisa {
 
 constexpr int kCacheThreads = 256;
-constexpr int kCacheRows = 4;  // rows in flight per thread
+constexpr int kCacheRows = 2;  // rows of K and of V in flight per thread
 
 struct CacheParams {
   Pages pages;
@@ -33,88 +32,134 @@ struct CacheParams {
   int64_t rows;  // B * Hkv * N
 };
 
-// cache row of token t of (b, h), or -1
+template <int D, bool E4M3>
+struct CacheCfg {
+  static constexpr int PER = E4M3 ? 16 : 8;        // values of a row per thread
+  static constexpr int LPR = D / PER;              // threads per row
+  static constexpr int ROWS = kCacheThreads / LPR; // rows of a CTA's step
+};
+
+// cache row of position `pos` of (b, h), or -1
 __device__ __forceinline__ int64_t cache_row(const CacheParams& p, int b, int h, int pos) {
   const int at = page_of(p.pages, b, pos);
   return at < 0 ? -1 : ((int64_t(at) * p.Hkv + h) << p.pages.log_page) + (pos & ((1 << p.pages.log_page) - 1));
 }
 
-// 8 bf16 (one 16-byte load) -> the row's scale and 8 codes
-template <int D>
-__device__ __forceinline__ uint2 quantise8(const uint4& x, float& scale) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// four quotients -> four codes
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3)) |
+         uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16;
+}
+
+// 16 bf16 of a row -> its scale and 16 codes.
+// x * (1 / scale) is within two fp32 steps of the quotient, so both round to the same code
+// unless a tie lies between them. Ties of e4m3 (3 mantissa bits) have the low 20 bits of the
+// fp32 mantissa 0x80000; below 2^-6 the codes' step stays 2^-9, as it is in [2^-6, 2^-5), so
+// 2^-6 is added there first. Only a row that comes within four steps of a tie divides.
+template <int LPR>
+__device__ __forceinline__ uint4 quantise16(const uint4& x0, const uint4& x1, float& scale) {
+  const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+  for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
 #pragma unroll
-  for (int off = 1; off < D / 8; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+  for (int off = 1; off < LPR; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
   if (top >= 0x7f80u) top = 0x7fc0u;  // an infinity or a NaN: NaN for the row
   scale = __fdiv_rn(__uint_as_float(top << 16), 448.f);
   if (scale < 1.17549435e-38f) scale = 1.17549435e-38f;  // a NaN stays one
-  uint32_t c[2];
+  const float inv = __frcp_rn(scale);
+  float f[16];
+  bool near = false;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 f = make_float4(__fdiv_rn(bf16_lo(w[2 * i]), scale), __fdiv_rn(bf16_hi(w[2 * i]), scale),
-                                 __fdiv_rn(bf16_lo(w[2 * i + 1]), scale), __fdiv_rn(bf16_hi(w[2 * i + 1]), scale));
-    c[i] = uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(f.x, f.y), __NV_SATFINITE, __NV_E4M3)) |
-           uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(f.z, f.w), __NV_SATFINITE, __NV_E4M3)) << 16;
+  for (int i = 0; i < 16; ++i) {
+    f[i] = (i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1])) * inv;
+    const float a = fabsf(f[i]);
+    const uint32_t low = (__float_as_uint(a < 0.015625f ? a + 0.015625f : a) & 0xfffffu) - 0x80000u + 4u;
+    near |= low <= 8u;
   }
-  return make_uint2(c[0], c[1]);
+  if (near) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {  // rolled: rare, and its code should stay small
+      const uint32_t a = i == 0 ? w[0] : i == 1 ? w[2] : i == 2 ? w[4] : w[6];
+      const uint32_t b = i == 0 ? w[1] : i == 1 ? w[3] : i == 2 ? w[5] : w[7];
+      const float q0 = __fdiv_rn(bf16_lo(a), scale), q1 = __fdiv_rn(bf16_hi(a), scale);
+      const float q2 = __fdiv_rn(bf16_lo(b), scale), q3 = __fdiv_rn(bf16_hi(b), scale);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k == i) {
+          f[4 * k] = q0;
+          f[4 * k + 1] = q1;
+          f[4 * k + 2] = q2;
+          f[4 * k + 3] = q3;
+        }
+    }
+  }
+  return make_uint4(codes4(f[0], f[1], f[2], f[3]), codes4(f[4], f[5], f[6], f[7]), codes4(f[8], f[9], f[10], f[11]),
+                    codes4(f[12], f[13], f[14], f[15]));
 }
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheParams p) {
-  constexpr int LPR = D / 8;  // threads per row
-  const int part = threadIdx.x % LPR;
-  const int64_t step = int64_t(gridDim.x) * (kCacheThreads / LPR);
-  const int64_t first = int64_t(blockIdx.x) * (kCacheThreads / LPR) + threadIdx.x / LPR;
+  using C = CacheCfg<D, E4M3>;
+  constexpr int X = C::PER / 8;  // 16-byte loads of a row per thread
+  const int part = threadIdx.x % C::LPR, mine = threadIdx.x / C::LPR;
+  const int64_t step = int64_t(gridDim.x) * C::ROWS;
   // every thread of a warp takes the same number of rounds (the shuffles need all lanes)
-  for (int64_t r0 = first - threadIdx.x / LPR; r0 < p.rows; r0 += step * kCacheRows) {
-    uint4 k[kCacheRows], v[kCacheRows];
+  for (int64_t r0 = int64_t(blockIdx.x) * C::ROWS; r0 < p.rows; r0 += step * kCacheRows) {
+    uint4 k[kCacheRows][X], v[kCacheRows][X];
     int64_t to[kCacheRows];
+    // the values do not wait for the lengths and the table: a token that turns out not to be
+    // real is read all the same (it lies inside K and V)
 #pragma unroll
     for (int i = 0; i < kCacheRows; ++i) {
-      const int64_t r = r0 + threadIdx.x / LPR + i * step;
+      const int64_t r = r0 + mine + i * step;
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        k[i][x] = v[i][x] = make_uint4(0, 0, 0, 0);
+        if (r < p.rows) {
+          k[i][x] = ldg_stream_v4(p.K + r * D + part * C::PER + x * 8);
+          v[i][x] = ldg_stream_v4(p.V + r * D + part * C::PER + x * 8);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kCacheRows; ++i) {
+      const int64_t r = r0 + mine + i * step;
       to[i] = -1;
-      k[i] = v[i] = make_uint4(0, 0, 0, 0);
       if (r < p.rows) {
         const uint32_t bh = uint32_t(r) / uint32_t(p.N), t = uint32_t(r) % uint32_t(p.N);
         const int b = bh / p.Hkv, h = bh % p.Hkv;
         const int n = q_len_of(p.pages, b, p.N), pos = kv_len_of(p.pages, b) - n + int(t);
-        if (int(t) < n && pos >= 0) {
-          to[i] = cache_row(p, b, h, pos);
-          k[i] = ldg_stream_v4(p.K + r * D + part * 8);
-          v[i] = ldg_stream_v4(p.V + r * D + part * 8);
-        }
+        if (int(t) < n && pos >= 0) to[i] = cache_row(p, b, h, pos);
       }
     }
 #pragma unroll
     for (int i = 0; i < kCacheRows; ++i) {
       if constexpr (E4M3) {
         float ks, vs;
-        const uint2 kc = quantise8<D>(k[i], ks), vc = quantise8<D>(v[i], vs);
+        const uint4 kc = quantise16<C::LPR>(k[i][0], k[i][1], ks), vc = quantise16<C::LPR>(v[i][0], v[i][1], vs);
         if (to[i] >= 0) {
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.cK) + to[i] * D + part * 8) = kc;
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.cV) + to[i] * D + part * 8) = vc;
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.cK) + to[i] * D + part * 16) = kc;
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.cV) + to[i] * D + part * 16) = vc;
           if (part == 0) {
             p.ks[to[i]] = ks;
             p.vs[to[i]] = vs;
           }
         }
       } else if (to[i] >= 0) {
-        *reinterpret_cast<uint4*>(static_cast<bf16*>(p.cK) + to[i] * D + part * 8) = k[i];
-        *reinterpret_cast<uint4*>(static_cast<bf16*>(p.cV) + to[i] * D + part * 8) = v[i];
+        *reinterpret_cast<uint4*>(static_cast<bf16*>(p.cK) + to[i] * D + part * 8) = k[i][0];
+        *reinterpret_cast<uint4*>(static_cast<bf16*>(p.cV) + to[i] * D + part * 8) = v[i][0];
       }
     }
   }
 }
 
 // 8 codes and their scale -> 8 bf16
-__device__ __forceinline__ uint4 restore8(const uint2& c, float scale) {
+__device__ __forceinline__ uint4 restore8(uint32_t lo, uint32_t hi, float scale) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t two = e4m3x2_to_bf16x2(i < 2 ? c.x >> (16 * i) : c.y >> (16 * (i - 2)));
+    const uint32_t two = e4m3x2_to_bf16x2((i < 2 ? lo : hi) >> (16 * (i & 1)));
     w[i] = pack_bf16x2(bf16_lo(two) * scale, bf16_hi(two) * scale);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -122,47 +167,47 @@ __device__ __forceinline__ uint4 restore8(const uint2& c, float scale) {
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheParams p) {
-  constexpr int LPR = D / 8;
-  const int part = threadIdx.x % LPR;
-  const int64_t step = int64_t(gridDim.x) * (kCacheThreads / LPR);
-  const int64_t first = int64_t(blockIdx.x) * (kCacheThreads / LPR) + threadIdx.x / LPR;
-  for (int64_t r0 = first; r0 < p.rows; r0 += step * kCacheRows) {
+  using C = CacheCfg<D, E4M3>;
+  const int part = threadIdx.x % C::LPR;
+  const int64_t step = int64_t(gridDim.x) * C::ROWS;
+  for (int64_t r0 = int64_t(blockIdx.x) * C::ROWS + threadIdx.x / C::LPR; r0 < p.rows; r0 += step * kCacheRows) {
     uint4 k[kCacheRows], v[kCacheRows];
     float ks[kCacheRows], vs[kCacheRows];
-    bool held[kCacheRows];
+    int64_t from[kCacheRows];
 #pragma unroll
     for (int i = 0; i < kCacheRows; ++i) {
       const int64_t r = r0 + i * step;
-      int64_t from = -1;
+      from[i] = -1;
       if (r < p.rows) {
         const uint32_t bh = uint32_t(r) / uint32_t(p.N), t = uint32_t(r) % uint32_t(p.N);
         const int b = bh / p.Hkv, h = bh % p.Hkv;
-        if (int(t) < kv_len_of(p.pages, b)) from = cache_row(p, b, h, int(t));
-      }
-      held[i] = from >= 0;
-      if (!held[i]) continue;
-      if constexpr (E4M3) {
-        const uint2 a = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.pages.K) + from * D + part * 8));
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.pages.V) + from * D + part * 8));
-        k[i] = make_uint4(a.x, a.y, 0, 0);
-        v[i] = make_uint4(c.x, c.y, 0, 0);
-        ks[i] = __ldg(p.pages.ks + from);
-        vs[i] = __ldg(p.pages.vs + from);
-      } else {
-        k[i] = ldg_stream_v4(static_cast<const bf16*>(p.pages.K) + from * D + part * 8);
-        v[i] = ldg_stream_v4(static_cast<const bf16*>(p.pages.V) + from * D + part * 8);
+        if (int(t) < kv_len_of(p.pages, b)) from[i] = cache_row(p, b, h, int(t));
       }
     }
 #pragma unroll
     for (int i = 0; i < kCacheRows; ++i) {
-      if (!held[i]) continue;
-      const int64_t r = r0 + i * step;
+      if (from[i] < 0) continue;
+      k[i] = ldg_stream_v4(static_cast<const uint8_t*>(p.pages.K) + from[i] * (E4M3 ? D : 2 * D) + part * 16);
+      v[i] = ldg_stream_v4(static_cast<const uint8_t*>(p.pages.V) + from[i] * (E4M3 ? D : 2 * D) + part * 16);
       if constexpr (E4M3) {
-        k[i] = restore8(make_uint2(k[i].x, k[i].y), ks[i]);
-        v[i] = restore8(make_uint2(v[i].x, v[i].y), vs[i]);
+        ks[i] = __ldg(p.pages.ks + from[i]);
+        vs[i] = __ldg(p.pages.vs + from[i]);
       }
-      *reinterpret_cast<uint4*>(p.oK + r * D + part * 8) = k[i];
-      *reinterpret_cast<uint4*>(p.oV + r * D + part * 8) = v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kCacheRows; ++i) {
+      if (from[i] < 0) continue;
+      uint4* dk = reinterpret_cast<uint4*>(p.oK + (r0 + i * step) * D + part * C::PER);
+      uint4* dv = reinterpret_cast<uint4*>(p.oV + (r0 + i * step) * D + part * C::PER);
+      if constexpr (E4M3) {
+        dk[0] = restore8(k[i].x, k[i].y, ks[i]);
+        dk[1] = restore8(k[i].z, k[i].w, ks[i]);
+        dv[0] = restore8(v[i].x, v[i].y, vs[i]);
+        dv[1] = restore8(v[i].z, v[i].w, vs[i]);
+      } else {
+        dk[0] = k[i];
+        dv[0] = v[i];
+      }
     }
   }
 }

@@ -83,10 +83,10 @@ pisa_status_t check_cache(const pisa_cache_t& c, const pisa_sequences_t& s, int3
   return ok();
 }
 
-// the paged cache's kernels: a row per D/8 threads, kCacheRows rows in flight per thread
+// the paged cache's kernels: 16 bytes of a cache row per thread, rows dealt out to the CTAs in turn
 template <typename Kernel>
 pisa_status_t launch_cache(Kernel k, const pisa::CacheParams& p, int d, int sms, cudaStream_t st, const char* what) {
-  const int64_t per = int64_t(pisa::kCacheThreads) / (d / 8);
+  const int64_t per = int64_t(pisa::kCacheThreads) * (p.ks || p.pages.ks ? 16 : 8) / d;
   const int64_t ctas = (p.rows + per - 1) / per;
   const int64_t most = int64_t(sms) * 8;
   k<<<unsigned(ctas < most ? ctas : most), pisa::kCacheThreads, 0, st>>>(p);

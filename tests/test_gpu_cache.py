@@ -365,3 +365,22 @@ def test_table_rows_and_lengths_at_odd_offsets():
     Q = randn(3, 2, 1, 64, seed=90)
     a, b = P.paged_attention(Q, cache, big, n), P.paged_attention(Q, cache, table, n.clone())
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_codes_near_every_tie():
+    """Rows whose quotients fall on and beside ties of the rounding, over many scales: the codes
+    are those of the fp32 quotient."""
+    d, page = 128, 128
+    rng = np.random.default_rng(21)
+    x = np.zeros((128, d), np.float32)
+    for r in range(128):
+        amax = np.float32(rng.choice([448, 7, 1, 3.5, 0.21875, 1000, 2.0 ** -120, 57]) * (1 if r % 3 else rng.uniform(1, 2)))
+        scale = amax / 448
+        ties = rng.integers(0, 16, d) * 2.0 ** rng.integers(-10, 5, d) + 2.0 ** rng.integers(-10, 5, d)
+        x[r] = np.clip(ties, 0, 448) * scale * rng.choice([-1, 1], d)
+        x[r, 0] = amax
+    x = torch.from_numpy(x).to(BF16).cuda().view(1, 1, 128, d)
+    cache = P.paged_cache(1, 1, page, d, E4M3)
+    P.cache_write(x, x, cache, ints([[0]]), ints([128]))
+    code, scale = W.quantise_rows(f64(x)[0, 0])
+    assert np.array_equal(f64(cache.K)[0, 0], code) and np.array_equal(cache.k_scale[0, 0].cpu().numpy(), scale)

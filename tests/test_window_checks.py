@@ -156,10 +156,11 @@ def test_binding_refuses_wrong_tensors(L):
 def test_binding_refuses_wrong_caches(L):
     c = P.paged_cache(4, 2, 16, 64, E4M3, device="cpu")
     table, lens = torch.zeros(1, 3, dtype=I32), torch.zeros(1, dtype=I32)
-    cpu = torch.device("cpu")
 
     def args(cache=c, table=table, lens=lens, news=None):
-        return P._cache_args(cache, table, lens, news, 1, 8, cpu)
+        with pytest.raises(ValueError, match="CUDA"):  # host tensors: refused last
+            P._check_operands(P._cache_checks(cache, table, lens, news, 1))
+        return P._cache_args(cache, table, lens, news, 1, 8)
 
     a, s = args()
     assert (a.num_pages, a.Hkv, a.page, a.d, a.type, s.B, s.N, s.max_pages) == (4, 2, 16, 64, 1, 1, 8, 3)
@@ -169,8 +170,10 @@ def test_binding_refuses_wrong_caches(L):
            dict(lens=lens.long()), dict(lens=torch.zeros(2, dtype=I32)), dict(news=torch.zeros(1)),
            dict(table=torch.zeros(1, 6, dtype=I32)[:, ::2])]
     for kw in bad:
-        with pytest.raises(ValueError):
-            args(**kw)
+        a = dict(cache=c, table=table, lens=lens, news=None) | kw
+        with pytest.raises(ValueError) as e:
+            P._check_operands(P._cache_checks(a["cache"], a["table"], a["lens"], a["news"], 1))
+        assert "CUDA" not in str(e.value), kw
     with pytest.raises(ValueError, match="dtype"):
         P.paged_cache(4, 2, 16, 64, torch.float16, device="cpu")
     with pytest.raises(ValueError, match="CUDA"):
@@ -188,4 +191,5 @@ def test_binding_refuses_wrong_workspaces():
     for bad in (torch.zeros(8), torch.zeros(4, dtype=torch.uint8), torch.zeros(32, dtype=torch.uint8)[::2], "no"):
         with pytest.raises(ValueError, match="workspace"):
             P._workspace(bad, 16, cpu)
-    assert P._workspace(torch.zeros(16, dtype=torch.uint8), 16, cpu).numel() == 16
+    assert P._workspace(torch.zeros(16, dtype=torch.uint8), 16, cpu)[1] == 16
+    assert P._workspace(None, 0, cpu) == (None, 0, None)
