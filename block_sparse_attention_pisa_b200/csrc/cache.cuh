@@ -52,10 +52,12 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 }
 
 // 16 bf16 of a row -> its scale and 16 codes.
-// x * (1 / scale) is within two fp32 steps of the quotient, so both round to the same code
-// unless a tie lies between them. Ties of e4m3 (3 mantissa bits) have the low 20 bits of the
-// fp32 mantissa 0x80000; below 2^-6 the codes' step stays 2^-9, as it is in [2^-6, 2^-5), so
-// 2^-6 is added there first. Only a row that comes within four steps of a tie divides.
+// The fp32 quotient x / scale by Markstein's correction (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990): with y the correctly
+// rounded reciprocal and q = x y, the remainder r = x - q scale is exact and q + r y is the
+// correctly rounded quotient, unless scale's mantissa is all ones or r leaves the range. Rows
+// of such scales (below 2^-90 the remainder could) divide. Three operations a value; with a
+// division for each the kernel was bound by issue (75 us for 2 x 24 x 4096 rows of 128).
 template <int LPR>
 __device__ __forceinline__ uint4 quantise16(const uint4& x0, const uint4& x1, float& scale) {
   const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
@@ -67,35 +69,31 @@ __device__ __forceinline__ uint4 quantise16(const uint4& x0, const uint4& x1, fl
   if (top >= 0x7f80u) top = 0x7fc0u;  // an infinity or a NaN: NaN for the row
   scale = __fdiv_rn(__uint_as_float(top << 16), 448.f);
   if (scale < 1.17549435e-38f) scale = 1.17549435e-38f;  // a NaN stays one
-  const float inv = __frcp_rn(scale);
-  float f[16];
-  bool near = false;
+  const bool divide = scale < 8.0779357e-28f || (__float_as_uint(scale) & 0x7fffffu) == 0x7fffffu;
+  uint32_t c[4];
+  if (!divide) {
+    const float y = __frcp_rn(scale);
+    auto quotient = [&](float x) {
+      const float q = x * y;
+      return fmaf(fmaf(-q, scale, x), y, q);
+    };
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    f[i] = (i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1])) * inv;
-    const float a = fabsf(f[i]);
-    const uint32_t low = (__float_as_uint(a < 0.015625f ? a + 0.015625f : a) & 0xfffffu) - 0x80000u + 4u;
-    near |= low <= 8u;
-  }
-  if (near) {
+    for (int i = 0; i < 4; ++i)
+      c[i] = codes4(quotient(bf16_lo(w[2 * i])), quotient(bf16_hi(w[2 * i])), quotient(bf16_lo(w[2 * i + 1])),
+                    quotient(bf16_hi(w[2 * i + 1])));
+  } else {
 #pragma unroll 1
     for (int i = 0; i < 4; ++i) {  // rolled: rare, and its code should stay small
       const uint32_t a = i == 0 ? w[0] : i == 1 ? w[2] : i == 2 ? w[4] : w[6];
       const uint32_t b = i == 0 ? w[1] : i == 1 ? w[3] : i == 2 ? w[5] : w[7];
-      const float q0 = __fdiv_rn(bf16_lo(a), scale), q1 = __fdiv_rn(bf16_hi(a), scale);
-      const float q2 = __fdiv_rn(bf16_lo(b), scale), q3 = __fdiv_rn(bf16_hi(b), scale);
+      const uint32_t x = codes4(__fdiv_rn(bf16_lo(a), scale), __fdiv_rn(bf16_hi(a), scale), __fdiv_rn(bf16_lo(b), scale),
+                                __fdiv_rn(bf16_hi(b), scale));
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (k == i) {
-          f[4 * k] = q0;
-          f[4 * k + 1] = q1;
-          f[4 * k + 2] = q2;
-          f[4 * k + 3] = q3;
-        }
+        if (k == i) c[k] = x;
     }
   }
-  return make_uint4(codes4(f[0], f[1], f[2], f[3]), codes4(f[4], f[5], f[6], f[7]), codes4(f[8], f[9], f[10], f[11]),
-                    codes4(f[12], f[13], f[14], f[15]));
+  return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
 template <int D, bool E4M3>
