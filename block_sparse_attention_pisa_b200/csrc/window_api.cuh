@@ -187,7 +187,8 @@ pisa_status_t launch_token(const pisa::AttendTcParams& a, int ctas, void* worksp
   pisa::AttendTokenParams p{a.Q, a.O, a.lse, static_cast<float*>(workspace), nullptr, a.pages, a.B, a.Hq, a.Hkv, a.N,
                             ctas, a.win, a.scale};
   p.part_lse = p.part + size_t(2) * ctas * pisa::kTokenRows * D;
-  pisa::attend_token_kernel<D, E4M3><<<unsigned(ctas), 32 * pisa::kTokenWarps, 0, st>>>(p);
+  if constexpr (E4M3) pisa::attend_token8_kernel<D><<<unsigned(ctas), 32 * pisa::kTokenWarps, 0, st>>>(p);
+  else pisa::attend_token_kernel<D><<<unsigned(ctas), 32 * pisa::kTokenWarps, 0, st>>>(p);
   PISA_TRY(check_launch("attend_token_kernel"));
   // the join's blocks start while the pieces are still being computed, and wait for them
   cudaLaunchConfig_t cfg = {};

@@ -384,3 +384,23 @@ def test_codes_near_every_tie():
     P.cache_write(x, x, cache, ints([[0]]), ints([128]))
     code, scale = W.quantise_rows(f64(x)[0, 0])
     assert np.array_equal(f64(cache.K)[0, 0], code) and np.array_equal(cache.k_scale[0, 0].cpu().numpy(), scale)
+
+
+@pytest.mark.parametrize("N", [1, 40])
+def test_scales_of_every_size(N):
+    """Value rows whose scales differ by up to 2^60, key rows with codes down to the smallest, and
+    queries whose dimensions differ by 2^12: the weights keep their precision beside them."""
+    lens, d, page = [600, 77], 128, 32
+    rng = np.random.default_rng(31)
+    table, total = table_of(lens, page, seed=31)
+    cache = P.paged_cache(total, 2, page, d, E4M3)
+    x = torch.randn(2, 2, 600, d, generator=torch.Generator().manual_seed(31))
+    K = x.flip(2) * torch.from_numpy(rng.choice([1.0, 2.0 ** -7, 2.0 ** -12], (2, 2, 600, d))).float()
+    V = x * torch.from_numpy(2.0 ** rng.integers(-30, 31, (2, 2, 600, 1))).float()
+    P.cache_write(K.to(BF16).cuda(), V.to(BF16).cuda(), cache, table, ints(lens), ints(lens))
+    Q = torch.randn(2, 8, N, d, generator=torch.Generator().manual_seed(32)) * torch.from_numpy(
+        2.0 ** rng.integers(-12, 1, (2, 8, N, d))).float()
+    Q = (Q * 4).to(BF16).cuda()
+    O, lse = P.paged_attention(Q, cache, table, ints(lens))
+    P.device_error()
+    check_attention(O, lse, Q, cache, table, lens, [N] * 2, -1, 0, 0, d ** -0.5)
