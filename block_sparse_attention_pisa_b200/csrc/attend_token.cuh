@@ -32,6 +32,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "attend_tc.cuh"
 
 namespace pisa {
@@ -54,7 +56,7 @@ constexpr int kTokenWarps = 4;
 
 template <int D, bool E4M3>
 struct AttendTokenCfg {
-  static constexpr int KEYS = 4096 / (E4M3 ? D : 2 * D);  // of a warp's step: 4 KB of K and of V
+  static constexpr int KEYS = 2048 / D;  // of a warp's step: 16 at D = 128
   static constexpr int CHUNK = kTokenWarps * KEYS;
 };
 
@@ -239,38 +241,58 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 2) attend_token_kernel(const
       return s.see.any(j, 16) ? page_of(p.pages, b, j) : -1;
     };
     auto in = [&](int j) { return j < s.see.sk || (j >= s.see.lo && j < s.see.hi); };
-    auto load_k = [&](int c, int held) {
+    // `all`: every key of the step is seen by some row and held; otherwise rows that are not become 0
+    auto load_k = [&](int c, int held, auto all) {
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         const int page = __shfl_sync(0xffffffffu, held, i), j = s.key(c, CHUNK) + warp * KEYS + i * 16;
         const int64_t row = ((int64_t(page) * p.Hkv + hk) << p.pages.log_page) + (j & page_mask);
+        const bf16* src = static_cast<const bf16*>(p.pages.K) + (row + g) * D + q * 8;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const bool ok = page >= 0 && in(j + 8 * t + g);
+          const bool ok = all || (page >= 0 && in(j + 8 * t + g));
 #pragma unroll
-          for (int x = 0; x < KCH; ++x)
-            kr[i][t][x] = ldg16(static_cast<const uint8_t*>(p.pages.K) + (row + 8 * t + g) * (2 * D) + x * 64 + q * 16, ok);
+          for (int x = 0; x < KCH; ++x) {
+            if constexpr (all) kr[i][t][x] = ldg_stream_v4(src + 8 * t * D + x * 32);
+            else kr[i][t][x] = ldg16(src + 8 * t * D + x * 32, ok);
+          }
         }
       }
     };
-    auto load_v = [&](int c, int held) {
+    auto load_v = [&](int c, int held, auto all) {
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         const int page = __shfl_sync(0xffffffffu, held, i), j = s.key(c, CHUNK) + warp * KEYS + i * 16;
         const int64_t row = ((int64_t(page) * p.Hkv + hk) << p.pages.log_page) + (j & page_mask);
+        const bf16* src = static_cast<const bf16*>(p.pages.V) + (row + 2 * q) * D + g * 8;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {  // keys 2q, 2q + 1, 2q + 8, 2q + 9
-          const int key = 2 * q + (e & 1) + (e >> 1) * 8;
-          const bool ok = page >= 0 && in(j + key);
-          const uint8_t* src = static_cast<const uint8_t*>(p.pages.V) + (row + key) * (2 * D);
+          const int key = (e & 1) + (e >> 1) * 8;
+          const bool ok = all || (page >= 0 && in(j + 2 * q + key));
 #pragma unroll
-          for (int x = 0; x < VCH; ++x) vr[i][e][x] = ldg16(src + x * 128 + g * 16, ok);
+          for (int x = 0; x < VCH; ++x) {
+            if constexpr (all) vr[i][e][x] = ldg_stream_v4(src + key * D + x * 64);
+            else vr[i][e][x] = ldg16(src + key * D + x * 64, ok);
+          }
         }
       }
     };
+    auto full = [&](int c, int held) {
+      const int j = s.key(c, CHUNK) + warp * KEYS;
+      return (j + KEYS <= s.see.sk || (j >= s.see.lo && j + KEYS <= s.see.hi)) && __all_sync(0xffffffffu, lane >= NG || held >= 0);
+    };
+    const auto fetch_k = [&](int c, int held, bool all) {
+      if (all) load_k(c, held, std::true_type{});
+      else load_k(c, held, std::false_type{});
+    };
+    const auto fetch_v = [&](int c, int held, bool all) {
+      if (all) load_v(c, held, std::true_type{});
+      else load_v(c, held, std::false_type{});
+    };
     int held = pages_of(c0);
-    load_k(c0, held);
-    load_v(c0, held);
+    bool all = full(c0, held);
+    fetch_k(c0, held, all);
+    fetch_v(c0, held, all);
     int next = pages_of(c0 + 1);
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
@@ -289,10 +311,10 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 2) attend_token_kernel(const
             mma_bf16_16816(sc[i][t], qa[2 * x + 1], w[2], w[3]);
           }
         }
-      if (c + 1 < c1) load_k(c + 1, next);
-      const bool whole = j0 + KEYS - 1 <= s.see.p0 + p.win.right && j0 + KEYS <= s.n &&
-                         (j0 >= s.see.p1 - p.win.left || j0 + KEYS <= p.win.sinks) &&
-                         __all_sync(0xffffffffu, lane >= NG || held >= 0);
+      const bool next_all = full(c + 1, next);
+      if (c + 1 < c1) fetch_k(c + 1, next, next_all);
+      const bool whole = all && j0 + KEYS - 1 <= s.see.p0 + p.win.right &&
+                         (j0 >= s.see.p1 - p.win.left || j0 + KEYS <= p.win.sinks);
       if (!whole) {
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
@@ -364,8 +386,9 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 2) attend_token_kernel(const
           }
         }
       }
-      if (c + 1 < c1) load_v(c + 1, next);
+      if (c + 1 < c1) fetch_v(c + 1, next, next_all);
       held = next;
+      all = next_all;
       next = pages_of(c + 2);
     }
     // the warps' accumulators, joined in warp order
@@ -424,9 +447,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(32 * kTokenWarps, 2) attend_token8_kernel(const AttendTokenParams p) {
+__global__ void __launch_bounds__(32 * kTokenWarps, 3) attend_token8_kernel(const AttendTokenParams p) {
   using C = AttendTokenCfg<D, true>;
-  constexpr int KEYS = C::KEYS, NB = KEYS / 32, CHUNK = C::CHUNK;
+  constexpr int KEYS = C::KEYS, NG = KEYS / 16, CHUNK = C::CHUNK;
   constexpr int KCH = D / 64;  // 16-byte loads of a key per lane, four product steps each
   constexpr int W = D / 32;    // words of a value per lane
   __shared__ float acc[kTokenWarps][kTokenRows][D + 4];
@@ -495,14 +518,14 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 2) attend_token8_kernel(cons
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    // n-tile t of a block of 32 keys holds keys 8 t + gr as columns; the lane's weights belong to keys
-    // 8 t + 2 q + {0, 1}, so those are the rows of V that it loads
-    uint4 kr[NB][4][KCH];
-    uint32_t vr[NB][4][2][W];
-    float2 ks[NB][4], vs[NB][4];
+    // product column gr of n-tile t is key 8 t + gr of its group of 16; the lane's weights belong to
+    // keys 8 t + 2 q + {0, 1}, so those are the rows of V that it loads
+    uint4 kr[NG][2][KCH];
+    uint32_t vr[NG][2][2][W];
+    float2 ks[NG][2], vs[NG][2];
     // lane i: the page of the step's i-th group of 16 keys, -1 if none of them is seen or held
     auto pages_of = [&](int c) -> int {
-      if (lane >= 2 * NB || c >= c1) return -1;
+      if (lane >= NG || c >= c1) return -1;
       const int j = s.key(c, CHUNK) + warp * KEYS + lane * 16;
       return s.see.any(j, 16) ? page_of(p.pages, b, j) : -1;
     };
@@ -510,61 +533,81 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 2) attend_token8_kernel(cons
     auto row_of = [&](int page, int j) {
       return ((int64_t(page) * p.Hkv + hk) << p.pages.log_page) + (j & page_mask);
     };
-    auto load_k = [&](int c, int held) {
+    // `all`: every key of the step is seen by some row and held; otherwise rows that are not become 0
+    auto load_k = [&](int c, int held, auto all) {
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+      for (int i = 0; i < NG; ++i) {
+        const int page = __shfl_sync(0xffffffffu, held, i), j = s.key(c, CHUNK) + warp * KEYS + i * 16;
+        const int64_t row = row_of(page, j);
+        const uint8_t* src = static_cast<const uint8_t*>(p.pages.K) + (row + gr) * D + q * 16;
+        const float* sp = p.pages.ks + row + 2 * q;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int page = __shfl_sync(0xffffffffu, held, 2 * i + (t >> 1));
-          const int j = s.key(c, CHUNK) + warp * KEYS + i * 32 + t * 8;
-          const int64_t row = row_of(page, j);
-          const bool ok = page >= 0 && in(j + gr);
+        for (int t = 0; t < 2; ++t) {
+          const bool ok = all || (page >= 0 && in(j + 8 * t + gr));
 #pragma unroll
-          for (int x = 0; x < KCH; ++x)
-            kr[i][t][x] = ldg16(static_cast<const uint8_t*>(p.pages.K) + (row + gr) * D + x * 64 + q * 16, ok);
-          ks[i][t] = page >= 0 ? __ldg(reinterpret_cast<const float2*>(p.pages.ks + row + 2 * q)) : make_float2(0.f, 0.f);
+          for (int x = 0; x < KCH; ++x) {
+            if constexpr (all) kr[i][t][x] = ldg_stream_v4(src + 8 * t * D + x * 64);
+            else kr[i][t][x] = ldg16(src + 8 * t * D + x * 64, ok);
+          }
+          ks[i][t] = all || page >= 0 ? __ldg(reinterpret_cast<const float2*>(sp + 8 * t)) : make_float2(0.f, 0.f);
         }
+      }
     };
-    auto load_v = [&](int c, int held) {
+    auto load_v = [&](int c, int held, auto all) {
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+      for (int i = 0; i < NG; ++i) {
+        const int page = __shfl_sync(0xffffffffu, held, i), j = s.key(c, CHUNK) + warp * KEYS + i * 16 + 2 * q;
+        const int64_t row = row_of(page, j);
+        const uint8_t* src = static_cast<const uint8_t*>(p.pages.V) + row * D + gr * (D / 8);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int page = __shfl_sync(0xffffffffu, held, 2 * i + (t >> 1));
-          const int j = s.key(c, CHUNK) + warp * KEYS + i * 32 + t * 8 + 2 * q;
-          const int64_t row = row_of(page, j);
-          const bool ok[2] = {page >= 0 && in(j), page >= 0 && in(j + 1)};
+        for (int t = 0; t < 2; ++t) {
+          const bool ok[2] = {all || (page >= 0 && in(j + 8 * t)), all || (page >= 0 && in(j + 8 * t + 1))};
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint8_t* src = static_cast<const uint8_t*>(p.pages.V) + (row + e) * D + gr * (D / 8);
             if constexpr (D == 128) {
-              const uint4 w = ldg16(src, ok[e]);
+              uint4 w;
+              if constexpr (all) w = ldg_stream_v4(src + (8 * t + e) * D);
+              else w = ldg16(src + (8 * t + e) * D, ok[e]);
               vr[i][t][e][0] = w.x;
               vr[i][t][e][1] = w.y;
               vr[i][t][e][W - 2] = w.z;
               vr[i][t][e][W - 1] = w.w;
             } else {
-              const uint2 w = ok[e] ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0, 0);
+              const uint2 w = ok[e] ? __ldg(reinterpret_cast<const uint2*>(src + (8 * t + e) * D)) : make_uint2(0, 0);
               vr[i][t][e][0] = w.x;
               vr[i][t][e][1] = w.y;
             }
           }
-          const float2 x = page >= 0 ? __ldg(reinterpret_cast<const float2*>(p.pages.vs + row)) : make_float2(0.f, 0.f);
+          const float2 x = all || page >= 0 ? __ldg(reinterpret_cast<const float2*>(p.pages.vs + row + 8 * t)) : make_float2(0.f, 0.f);
           vs[i][t] = make_float2(ok[0] ? x.x : 0.f, ok[1] ? x.y : 0.f);
         }
+      }
+    };
+    auto full = [&](int c, int held) {
+      const int j = s.key(c, CHUNK) + warp * KEYS;
+      return (j + KEYS <= s.see.sk || (j >= s.see.lo && j + KEYS <= s.see.hi)) && __all_sync(0xffffffffu, lane >= NG || held >= 0);
+    };
+    const auto fetch_k = [&](int c, int held, bool all) {
+      if (all) load_k(c, held, std::true_type{});
+      else load_k(c, held, std::false_type{});
+    };
+    const auto fetch_v = [&](int c, int held, bool all) {
+      if (all) load_v(c, held, std::true_type{});
+      else load_v(c, held, std::false_type{});
     };
     int held = pages_of(c0);
-    load_k(c0, held);
-    load_v(c0, held);
+    bool all = full(c0, held);
+    fetch_k(c0, held, all);
+    fetch_v(c0, held, all);
     int next = pages_of(c0 + 1);
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
       const int j0 = s.key(c, CHUNK) + warp * KEYS;
-      float sc[NB][4][4];
+      float sc[NG][2][4];
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+      for (int i = 0; i < NG; ++i)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < 2; ++t) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[i][t][e] = 0.f;
 #pragma unroll
@@ -579,31 +622,31 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 2) attend_token8_kernel(cons
           sc[i][t][2] *= ks[i][t].x;
           sc[i][t][3] *= ks[i][t].y;
         }
-      if (c + 1 < c1) load_k(c + 1, next);
-      const bool whole = j0 + KEYS - 1 <= s.see.p0 + p.win.right && j0 + KEYS <= s.n &&
-                         (j0 >= s.see.p1 - p.win.left || j0 + KEYS <= p.win.sinks) &&
-                         __all_sync(0xffffffffu, lane >= 2 * NB || held >= 0);
+      const bool next_all = full(c + 1, next);
+      if (c + 1 < c1) fetch_k(c + 1, next, next_all);
+      const bool whole = all && j0 + KEYS - 1 <= s.see.p0 + p.win.right &&
+                         (j0 >= s.see.p1 - p.win.left || j0 + KEYS <= p.win.sinks);
       if (!whole) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+        for (int i = 0; i < NG; ++i) {
+          const bool here = __shfl_sync(0xffffffffu, held, i) >= 0;
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const bool here = __shfl_sync(0xffffffffu, held, 2 * i + (t >> 1)) >= 0;
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int j = j0 + i * 32 + t * 8 + 2 * q + (e & 1), h = e >> 1;
+              const int j = j0 + i * 16 + t * 8 + 2 * q + (e & 1), h = e >> 1;
               if (!(here && j <= z[h] && (j >= a[h] || j < p.win.sinks))) sc[i][t][e] = -INFINITY;
             }
-          }
+        }
       }
       float old[2], tm[2] = {0.f, 0.f};  // g in the new frame of m, before it is bounded; largest weight
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+        for (int i = 0; i < NG; ++i)
 #pragma unroll
-          for (int t = 0; t < 4; ++t) mx = fmaxf(mx, fmaxf(sc[i][t][2 * h], sc[i][t][2 * h + 1]));
+          for (int t = 0; t < 2; ++t) mx = fmaxf(mx, fmaxf(sc[i][t][2 * h], sc[i][t][2 * h + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * sl2[h];
         old[h] = f[h];
@@ -617,9 +660,9 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 2) attend_token8_kernel(cons
       }
       const float neg[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+      for (int i = 0; i < NG; ++i)
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int h = e >> 1;
@@ -649,29 +692,26 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 2) attend_token8_kernel(cons
         }
       }
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        uint32_t pa[2][4];  // two halves of 16 keys
+      for (int i = 0; i < NG; ++i) {
+        uint32_t pa[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            pa[t >> 1][2 * (t & 1) + h] = pack_f16x2(sc[i][t][2 * h] * f[h], sc[i][t][2 * h + 1] * f[h]);
+          for (int h = 0; h < 2; ++h) pa[2 * t + h] = pack_f16x2(sc[i][t][2 * h] * f[h], sc[i][t][2 * h + 1] * f[h]);
         // byte e of word x of the lane's codes is column gr of product 4 x + e: d = gr D/8 + 4 x + e
 #pragma unroll
-        for (int x = 0; x < W; ++x)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t r0 = vr[i][2 * y][0][x], r1 = vr[i][2 * y][1][x], r2 = vr[i][2 * y + 1][0][x], r3 = vr[i][2 * y + 1][1][x];
-            const uint32_t lo0 = __byte_perm(r0, r1, 0x5140), hi0 = __byte_perm(r0, r1, 0x7362);
-            const uint32_t lo1 = __byte_perm(r2, r3, 0x5140), hi1 = __byte_perm(r2, r3, 0x7362);
-            mma_f16_16816(o[4 * x], pa[y], codes_to_f16_lo(lo0), codes_to_f16_lo(lo1));
-            mma_f16_16816(o[4 * x + 1], pa[y], codes_to_f16_hi(lo0), codes_to_f16_hi(lo1));
-            mma_f16_16816(o[4 * x + 2], pa[y], codes_to_f16_lo(hi0), codes_to_f16_lo(hi1));
-            mma_f16_16816(o[4 * x + 3], pa[y], codes_to_f16_hi(hi0), codes_to_f16_hi(hi1));
-          }
+        for (int x = 0; x < W; ++x) {
+          const uint32_t lo0 = __byte_perm(vr[i][0][0][x], vr[i][0][1][x], 0x5140), hi0 = __byte_perm(vr[i][0][0][x], vr[i][0][1][x], 0x7362);
+          const uint32_t lo1 = __byte_perm(vr[i][1][0][x], vr[i][1][1][x], 0x5140), hi1 = __byte_perm(vr[i][1][0][x], vr[i][1][1][x], 0x7362);
+          mma_f16_16816(o[4 * x], pa, codes_to_f16_lo(lo0), codes_to_f16_lo(lo1));
+          mma_f16_16816(o[4 * x + 1], pa, codes_to_f16_hi(lo0), codes_to_f16_hi(lo1));
+          mma_f16_16816(o[4 * x + 2], pa, codes_to_f16_lo(hi0), codes_to_f16_lo(hi1));
+          mma_f16_16816(o[4 * x + 3], pa, codes_to_f16_hi(hi0), codes_to_f16_hi(hi1));
+        }
       }
-      if (c + 1 < c1) load_v(c + 1, next);
+      if (c + 1 < c1) fetch_v(c + 1, next, next_all);
       held = next;
+      all = next_all;
       next = pages_of(c + 2);
     }
     // the warps' accumulators, joined in warp order

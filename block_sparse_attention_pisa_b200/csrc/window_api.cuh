@@ -172,14 +172,15 @@ pisa::AttendTcParams paged_plan(const pisa_cache_t& c, const pisa_sequences_t& s
   return a;
 }
 
-// Up to 16 rows per key head: the token kernel. Two CTAs per SM, fewer if the cache cannot
-// hold as many chunks.
+// Up to 16 rows per key head: the token kernel. As many CTAs as the SMs hold at once, fewer if
+// the cache cannot hold as many chunks.
 bool few_rows(const pisa::AttendTcParams& a) { return int64_t(a.Hq / a.Hkv) * a.N <= pisa::kTokenRows; }
-int token_ctas(const pisa::AttendTcParams& a, int64_t keys, int chunk) {
-  const int64_t most = int64_t(a.B) * a.Hkv * ((keys + chunk - 1) / chunk + 1);
-  return int(most < 2 * kSms ? most : 2 * kSms);
+int token_chunk(int d) { return pisa::kTokenWarps * 2048 / d; }
+int token_ctas(const pisa::AttendTcParams& a, int64_t keys, int d, int type) {
+  const int64_t chunk = token_chunk(d), most = int64_t(a.B) * a.Hkv * ((keys + chunk - 1) / chunk + 1);
+  const int64_t fit = (type == PISA_CACHE_E4M3 ? 3 : 2) * kSms;
+  return int(most < fit ? most : fit);
 }
-int token_chunk(int d, int type) { return pisa::kTokenWarps * 4096 / (type == PISA_CACHE_E4M3 ? d : 2 * d); }
 size_t token_workspace(int ctas, int d) { return size_t(2) * ctas * pisa::kTokenRows * (size_t(d) + 1) * 4; }
 
 template <int D, bool E4M3>
@@ -401,7 +402,7 @@ pisa_status_t pisa_paged_attention_workspace(pisa_cache_t cache, pisa_sequences_
   if (empty) return ok();
   int64_t keys = 0;
   const pisa::AttendTcParams a = paged_plan(cache, seqs, Hq, g, w, &keys);
-  *bytes = few_rows(a) ? token_workspace(token_ctas(a, keys, token_chunk(cache.d, cache.type)), cache.d)
+  *bytes = few_rows(a) ? token_workspace(token_ctas(a, keys, cache.d, cache.type), cache.d)
                        : attend_workspace(a, cache.d);
   return ok();
 }
@@ -433,7 +434,7 @@ pisa_status_t pisa_paged_attention(const void* Q, pisa_cache_t cache, pisa_seque
   auto st = static_cast<cudaStream_t>(stream);
   const bool codes = cache.type == PISA_CACHE_E4M3;
   if (few_rows(a)) {
-    const int ctas = token_ctas(a, keys, token_chunk(cache.d, cache.type));
+    const int ctas = token_ctas(a, keys, cache.d, cache.type);
     if (codes)
       return cache.d == 128 ? launch_token<128, true>(a, ctas, workspace, st) : launch_token<64, true>(a, ctas, workspace, st);
     return cache.d == 128 ? launch_token<128, false>(a, ctas, workspace, st) : launch_token<64, false>(a, ctas, workspace, st);
