@@ -175,11 +175,13 @@ pisa::AttendTcParams paged_plan(const pisa_cache_t& c, const pisa_sequences_t& s
 // Up to 16 rows per key head: the token kernel. As many CTAs as the SMs hold at once, fewer if
 // the cache cannot hold as many chunks.
 bool few_rows(const pisa::AttendTcParams& a) { return int64_t(a.Hq / a.Hkv) * a.N <= pisa::kTokenRows; }
-int token_chunk(int d) { return pisa::kTokenWarps * 2048 / d; }
 int token_ctas(const pisa::AttendTcParams& a, int64_t keys, int d, int type) {
-  const int64_t chunk = token_chunk(d), most = int64_t(a.B) * a.Hkv * ((keys + chunk - 1) / chunk + 1);
-  const int64_t fit = (type == PISA_CACHE_E4M3 ? 3 : 2) * kSms;
-  return int(most < fit ? most : fit);
+  const int64_t chunk = pisa::kTokenWarps * pisa::token_keys(d);
+  const int64_t most = int64_t(a.B) * a.Hkv * ((keys + chunk - 1) / chunk + 1);
+  const bool wide = int64_t(a.Hq / a.Hkv) * a.N > 8, codes = type == PISA_CACHE_E4M3;
+  const int fit = wide ? (codes ? pisa::token_ctas_per_sm<128, true, 2>() : pisa::token_ctas_per_sm<128, false, 2>())
+                       : (codes ? pisa::token_ctas_per_sm<128, true, 1>() : pisa::token_ctas_per_sm<128, false, 1>());
+  return int(most < int64_t(fit) * kSms ? most : int64_t(fit) * kSms);
 }
 size_t token_workspace(int ctas, int d) { return size_t(2) * ctas * pisa::kTokenRows * (size_t(d) + 1) * 4; }
 
@@ -188,12 +190,13 @@ pisa_status_t launch_token(const pisa::AttendTcParams& a, int ctas, void* worksp
   pisa::AttendTokenParams p{a.Q, a.O, a.lse, static_cast<float*>(workspace), nullptr, a.pages, a.B, a.Hq, a.Hkv, a.N,
                             ctas, a.win, a.scale};
   p.part_lse = p.part + size_t(2) * ctas * pisa::kTokenRows * D;
-  if constexpr (E4M3) pisa::attend_token8_kernel<D><<<unsigned(ctas), 32 * pisa::kTokenWarps, 0, st>>>(p);
-  else pisa::attend_token_kernel<D><<<unsigned(ctas), 32 * pisa::kTokenWarps, 0, st>>>(p);
+  const int64_t rows = int64_t(a.Hq / a.Hkv) * a.N;
+  auto k = rows > 8 ? pisa::attend_token_kernel<D, E4M3, 2> : pisa::attend_token_kernel<D, E4M3, 1>;
+  k<<<unsigned(ctas), 32 * pisa::kTokenWarps, 0, st>>>(p);
   PISA_TRY(check_launch("attend_token_kernel"));
   // the join's blocks start while the pieces are still being computed, and wait for them
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(a.B) * unsigned(a.Hkv));
+  cfg.gridDim = dim3(unsigned(a.B * a.Hkv * rows));
   cfg.blockDim = dim3(32 * pisa::kTokenWarps);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -201,7 +204,7 @@ pisa_status_t launch_token(const pisa::AttendTcParams& a, int ctas, void* worksp
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, pisa::attend_token_join_kernel<D, E4M3>, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, pisa::attend_token_join_kernel<D>, p);
   if (e != cudaSuccess) return fail(PISA_ERR_CUDA, "attend_token_join_kernel launch: %s", cudaGetErrorString(e));
   return check_launch("attend_token_join_kernel");
 }
