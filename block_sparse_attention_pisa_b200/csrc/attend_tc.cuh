@@ -3,19 +3,19 @@
 //
 //   o = sum_j exp(s_j - m) v_j / l,  l = sum_j exp(s_j - m),  s_j = scale q.k_j, j visible
 //
-// one pass over the keys with a running maximum m and sum l per row. The rows of a key head
-// are its G = Hq / Hkv query heads' tokens, token-major (row r = token r / G, head r % G), so
-// that shared keys are read once for all of them and a tile of rows spans few positions.
+// one pass over the keys with a running maximum m and sum l per row.
 //
-// A CTA takes two tiles (groups) of 128 rows of one key head and walks the 128-key tiles that
-// some row of theirs sees (the tiles of the first tokens, then the window's); a group skips
-// the ones that none of its rows sees. Warp roles:
-//   warp 0       producer: K and V tiles by TMA (a page at a time in a paged cache) into a ring;
+// A persistent CTA per SM takes items in turn: two tiles (groups) of 128 rows of one key head
+// that walk the 128-key tiles that some row of theirs sees (the tiles of the first tokens, then the
+// window's); a group skips the ones that none of its rows sees. Warp roles:
+//   warp 0       producer: K and V tiles by TMA (a page at a time in a paged cache) into a ring,
+//                running ahead into the next item;
 //   warp 1       one thread issues every tcgen05.mma: per tile and group S = Q K^T (SS), then
 //                O += P V (TS, P from tensor memory);
-//   warps 2-3    paged caches: clear the rows of a V tile that no row may see (unwritten rows
-//                may hold anything, and 0 x NaN is NaN); 8 bits: convert codes to bf16;
-//   warps 4-11   softmax: one thread per row (group = warps 4-7 or 8-11).
+//   warp 3       loads the next item's queries once the last scores of this one are done;
+//   warp 2       paged caches: clears the rows of a V tile that no row may see (unwritten rows
+//                may hold anything, and 0 x NaN is NaN); 8 bits: warps 2-3 convert codes to bf16;
+//   warps 4-11   softmax: one thread per row (group = warps 4-7 or 8-11), and the rows' output.
 // Tensor memory: S of either group (128 columns each, P in bf16 over the first half of its own
 // S) and O of either group (D columns each).
 //
@@ -34,6 +34,18 @@
 
 namespace pisa {
 
+// A tile of 128 rows holds `tokens` consecutive tokens of all query heads of a key head (of up to
+// 128 of them), head by head: row r is head r / tokens, token r % tokens. Shared keys are read once
+// for all their heads, and a tile spans few positions. One box of a [heads][tokens][D] tensor
+// map is such a tile; with a group that does not divide 128 a few rows stay idle (3 heads: 2).
+struct RowTiles {
+  int tokens, heads, parts;  // heads of a tile; tiles that a group's heads take
+  __host__ __device__ static RowTiles of(int G) {
+    const int h = G < 128 ? G : 128;
+    return RowTiles{128 / h, h, (G + 127) / 128};
+  }
+};
+
 struct AttendTcParams {
   const bf16* Q;
   bf16* O;
@@ -42,8 +54,10 @@ struct AttendTcParams {
   float* part_lse;
   Pages pages;      // paged only
   int B, Hq, Hkv, N;
-  int pairs;        // CTAs along a key head's rows
-  int splits;       // runs that a CTA's tile list is cut into
+  RowTiles rt;
+  int pairs;        // pairs of row tiles of a key head
+  int splits;       // runs that a piece's tile list is cut into
+  int items;        // pairs * B * Hkv * splits
   Window win;
   float scale;
 };
@@ -65,10 +79,12 @@ struct AttendTcCfg {
   static constexpr int B_LAND = B_EMPTY + NS;       // [NL] paged: copies landed, rows not cleared yet
   static constexpr int B_LEMPTY = B_LAND + NL;      // [NL] 8 bits: codes converted (2 warps)
   static constexpr int B_Q = B_LEMPTY + NL;         // [2] a group's queries are in shared memory
-  static constexpr int B_S = B_Q + 2;               // [2] S ready (commit)
+  static constexpr int B_QEMPTY = B_Q + 2;          // [2] the item's last scores are done (commit)
+  static constexpr int B_S = B_QEMPTY + 2;          // [2] S ready (commit)
   static constexpr int B_P = B_S + 2;               // [2] P written (4 warps)
-  static constexpr int B_O = B_P + 2;               // all products done (commit)
-  static constexpr int NBARS = B_O + 1;
+  static constexpr int B_O = B_P + 2;               // [2] the item's last product is done (commit)
+  static constexpr int B_END = B_O + 2;             // all products done (commit)
+  static constexpr int NBARS = B_END + 1;
   static constexpr int OFF_BAR = OFF_SCALE + (CODES ? 8 * 2 * 128 * 4 : 0);
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBARS;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
@@ -122,10 +138,59 @@ __device__ __forceinline__ uint32_t held_pages(const Pages& g, int b, const Sigh
   return __ballot_sync(0xffffffffu, ok);
 }
 
+// One piece of work: two tiles of a key head's rows over one run of their key tiles.
+struct AttendItem {
+  int b, hk, bh, split, n, nq;
+  int t0[2], head0, heads;  // first token of either tile; first query head and how many are real
+  Sight see[2], both;
+  TileList tiles;
+  bool real;
+};
+template <int KV>
+__device__ __forceinline__ AttendItem attend_item(const AttendTcParams& p, int id) {
+  AttendItem w;
+  const int G = p.Hq / p.Hkv;
+  int pair = id % p.pairs;
+  id /= p.pairs;
+  w.split = id % p.splits;
+  w.bh = id / p.splits;
+  w.b = w.bh / p.Hkv;
+  w.hk = w.bh - w.b * p.Hkv;
+  w.n = w.nq = p.N;
+  if constexpr (KV != kKvPlain) {
+    w.n = kv_len_of(p.pages, w.b);
+    w.nq = q_len_of(p.pages, w.b, p.N);
+  }
+  int part = 0;
+  const int per = p.pairs / p.rt.parts;
+  if (p.rt.parts > 1) {
+    part = pair / per;
+    pair -= part * per;
+  }
+  pair = per - 1 - pair;  // causal: the rows with the most keys first
+  w.head0 = w.b * p.Hq + w.hk * G + part * 128;
+  w.heads = min(p.rt.heads, G - part * 128);
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    w.t0[g] = (2 * pair + g) * p.rt.tokens;
+    if (w.t0[g] < w.nq) w.see[g].set(p.win, w.n - w.nq + w.t0[g], w.n - w.nq + min(w.t0[g] + p.rt.tokens, w.nq) - 1, w.n);
+    else w.see[g].none();
+  }
+  w.real = w.t0[0] < w.nq;
+  w.both = w.see[0];
+  if (w.see[1].hi > 0) {
+    w.both.lo = w.see[0].hi > 0 ? min(w.see[0].lo, w.see[1].lo) : w.see[1].lo;
+    w.both.hi = max(w.see[0].hi, w.see[1].hi);
+    w.both.sk = max(w.see[0].sk, w.see[1].sk);
+  }
+  w.tiles.set(w.both, w.split, p.splits);
+  return w;
+}
+
 template <int D, int KV>
 __global__ void __launch_bounds__(384, 1)
-attend_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                 const AttendTcParams p) {
+attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const AttendTcParams p) {
   using C = AttendTcCfg<D, KV>;
   using namespace tc;
   extern __shared__ __align__(16) uint8_t attend_smem[];
@@ -136,37 +201,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const uint32_t bar0 = base_u + C::OFF_BAR;
 #define ABAR(i) (bar0 + 8u * uint32_t(i))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  // ---- which rows, which keys: the same for every thread
-  const int G = p.Hq / p.Hkv;
-  int id = blockIdx.x;
-  const int pair = p.pairs - 1 - id % p.pairs;  // causal: the rows with the most keys first
-  id /= p.pairs;
-  const int split = id % p.splits, bh = id / p.splits;
-  const int b = bh / p.Hkv, hk = bh % p.Hkv;
-  int n = p.N, nq = p.N;
-  if constexpr (KV != kKvPlain) {
-    n = kv_len_of(p.pages, b);
-    nq = q_len_of(p.pages, b, p.N);
-  }
-  const int rows = nq * G;  // fits: B * Hq * N does
-  const int row0 = pair * 256;
-  if (row0 >= rows) return;
-  Sight see[2], both;
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const int a = row0 + 128 * g, z = min(a + 127, rows - 1);
-    if (a < rows) see[g].set(p.win, n - nq + a / G, n - nq + z / G, n);
-    else see[g].none();
-  }
-  both = see[0];
-  if (see[1].hi > 0) {
-    both.lo = see[0].hi > 0 ? min(see[0].lo, see[1].lo) : see[1].lo;
-    both.hi = max(see[0].hi, see[1].hi);
-    both.sk = max(see[0].sk, see[1].sk);
-  }
-  TileList tiles;
-  tiles.set(both, split, p.splits);
+  const int items = p.items, step = int(gridDim.x);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
@@ -178,11 +213,13 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       mbar_init(ABAR(C::B_LEMPTY + s), 2);
     }
     for (int g = 0; g < 2; ++g) {
-      mbar_init(ABAR(C::B_Q + g), 4);
+      mbar_init(ABAR(C::B_Q + g), 1);
+      mbar_init(ABAR(C::B_QEMPTY + g), 1);
       mbar_init(ABAR(C::B_S + g), 1);
       mbar_init(ABAR(C::B_P + g), 4);
+      mbar_init(ABAR(C::B_O + g), 1);
     }
-    mbar_init(ABAR(C::B_O), 1);
+    mbar_init(ABAR(C::B_END), 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -195,46 +232,50 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
 
+  // Every role walks the CTA's items; counters of ring stages and barrier phases run on.
   if (warp == 0) {
     // ------------------------------------------------------------- producer
-    // Lanes 0 and 1 issue the two 64-column panels of a tile (D = 64: lane 0 alone); stage use
-    // 2 i holds K of the run's i-th tile, 2 i + 1 its V.
+    // Lanes 0 and 1 issue the two 64-column panels of a tile (D = 64: lane 0 alone); of an item's
+    // i-th tile, K is stage use 2 i and V 2 i + 1 behind the items before.
     if (lane < 2) {
       bool ok = true;
       int use = 0;
-      for (int i = tiles.from; i < tiles.to && ok; ++i) {
-        const int j0 = tiles.key(i);
-        for (int kv = 0; kv < 2 && ok; ++kv, ++use) {
-          // the stage that the copies land in: the ring's, or one for codes
-          constexpr int NL = C::NL;
-          const int s = use % NL;
-          ok = wait_bounded(ABAR((C::CODES ? C::B_LEMPTY : C::B_EMPTY) + s), ((use / NL) & 1) ^ 1, abort_flag);
-          ok = __all_sync(0x3u, ok);
-          if (!ok) break;
-          const uint32_t dst = base_u + (C::CODES ? C::OFF_CODES + s * C::LAND : C::OFF_RING + s * C::TILE);
-          if constexpr (KV == kKvPlain) {
-            if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_FULL + s), C::TILE);
-            __syncwarp(0x3u);
-            if (lane * 64 < D)
-              tma_load_3d(dst + lane * 16384, kv ? &tmV : &tmK, ABAR(C::B_FULL + s), lane * 64, j0, bh);
-          } else {
-            // pages that no row of the CTA sees, or that the table does not hold, stay out
-            const int per = 128 >> p.pages.log_page, size = 1 << p.pages.log_page;
-            uint32_t held = 0;
-            for (int q = 0; q < per; ++q)
-              if (both.any(j0 + q * size, size) && page_of(p.pages, b, j0 + q * size) >= 0) held |= 1u << q;
-            if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_LAND + s), __popc(held) * size * D * (C::CODES ? 1 : 2));
-            __syncwarp(0x3u);
-            if constexpr (C::CODES) {  // whole rows of D codes, lanes by turns
-              for (int q = lane; q < per; q += 2)
-                if ((held >> q) & 1u)
-                  tma_load_3d(dst + q * size * D, kv ? &tmV : &tmK, ABAR(C::B_LAND + s), 0, 0,
-                              page_of(p.pages, b, j0 + q * size) * p.Hkv + hk);
-            } else if (lane * 64 < D) {
+      constexpr int NL = C::NL;  // the stages that the copies land in: the ring's, or those for codes
+      for (int id = blockIdx.x; id < items && ok; id += step) {
+        const AttendItem w = attend_item<KV>(p, id);
+        if (!w.real) continue;
+        for (int i = w.tiles.from; i < w.tiles.to && ok; ++i) {
+          const int j0 = w.tiles.key(i);
+          for (int kv = 0; kv < 2 && ok; ++kv, ++use) {
+            const int s = use % NL;
+            ok = wait_bounded(ABAR((C::CODES ? C::B_LEMPTY : C::B_EMPTY) + s), ((use / NL) & 1) ^ 1, abort_flag);
+            ok = __all_sync(0x3u, ok);
+            if (!ok) break;
+            const uint32_t dst = base_u + (C::CODES ? C::OFF_CODES + s * C::LAND : C::OFF_RING + s * C::TILE);
+            if constexpr (KV == kKvPlain) {
+              if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_FULL + s), C::TILE);
+              __syncwarp(0x3u);
+              if (lane * 64 < D)
+                tma_load_3d(dst + lane * 16384, kv ? &tmV : &tmK, ABAR(C::B_FULL + s), lane * 64, j0, w.bh);
+            } else {
+              // pages that no row of the CTA sees, or that the table does not hold, stay out
+              const int per = 128 >> p.pages.log_page, size = 1 << p.pages.log_page;
+              uint32_t held = 0;
               for (int q = 0; q < per; ++q)
-                if ((held >> q) & 1u)
-                  tma_load_3d(dst + lane * 16384 + q * size * 128, kv ? &tmV : &tmK, ABAR(C::B_LAND + s), lane * 64, 0,
-                              page_of(p.pages, b, j0 + q * size) * p.Hkv + hk);
+                if (w.both.any(j0 + q * size, size) && page_of(p.pages, w.b, j0 + q * size) >= 0) held |= 1u << q;
+              if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_LAND + s), __popc(held) * size * D * (C::CODES ? 1 : 2));
+              __syncwarp(0x3u);
+              if constexpr (C::CODES) {  // whole rows of D codes, lanes by turns
+                for (int q = lane; q < per; q += 2)
+                  if ((held >> q) & 1u)
+                    tma_load_3d(dst + q * size * D, kv ? &tmV : &tmK, ABAR(C::B_LAND + s), 0, 0,
+                                page_of(p.pages, w.b, j0 + q * size) * p.Hkv + w.hk);
+              } else if (lane * 64 < D) {
+                for (int q = 0; q < per; ++q)
+                  if ((held >> q) & 1u)
+                    tma_load_3d(dst + lane * 16384 + q * size * 128, kv ? &tmV : &tmK, ABAR(C::B_LAND + s), lane * 64, 0,
+                                page_of(p.pages, w.b, j0 + q * size) * p.Hkv + w.hk);
+              }
             }
           }
         }
@@ -242,300 +283,363 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       // no copy may still be in flight when the CTA exits
       constexpr int landed = KV == kKvPlain ? C::B_FULL : C::B_LAND;
       if (lane == 0)
-        for (int u = use > C::NL ? use - C::NL : 0; u < use; ++u) wait_drain(ABAR(landed + u % C::NL), (u / C::NL) & 1);
+        for (int u = use > NL ? use - NL : 0; u < use; ++u) wait_drain(ABAR(landed + u % NL), (u / NL) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- products
     if (lane == 0) {
       constexpr uint32_t idS = idesc_bf16(128, 128, false), idO = idesc_bf16(128, D, true);
       bool ok = true;
-      uint32_t has_o = 0, n_p = 0;  // bit g: O holds a product; phase of P
-      auto stage = [&](int use) { return base_u + C::OFF_RING + (use % C::NS) * C::TILE; };
-      auto full = [&](int use) { return wait_poll(ABAR(C::B_FULL + use % C::NS), (use / C::NS) & 1, abort_flag); };
-      auto scores = [&](int g, int i) {  // S = Q K^T of the run's i-th tile
-        const uint32_t q = base_u + C::OFF_Q + g * C::TILE, k = stage(2 * i);
+      uint32_t n_p = 0, n_q = 0;  // bit g: phase of P, of the queries
+      int use = 0;                // stage uses of the items before
+      auto stage = [&](int u) { return base_u + C::OFF_RING + (u % C::NS) * C::TILE; };
+      auto full = [&](int u) { return wait_poll(ABAR(C::B_FULL + u % C::NS), (u / C::NS) & 1, abort_flag); };
+      int id = blockIdx.x;
+      AttendItem w = attend_item<KV>(p, id);
+      while (id < items && ok) {
+        const int count = w.tiles.to - w.tiles.from;
+        uint32_t has_o = 0;  // bit g: O holds a product of this item
+        AttendItem next;
+        bool looked = false;
+        if (w.real) {
+          int last[2];  // a group's last tile of the run
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint32_t off = (c >> 2) * 16384 + (c & 3) * 32;
-          umma_ss(tmem + C::S_COL + g * 128, sdesc_sw128(q + off, 16, 1024), sdesc_sw128(k + off, 16, 1024), idS,
-                  c ? 1u : 0u);
+          for (int g = 0; g < 2; ++g) {
+            last[g] = count - 1;
+            while (last[g] >= 0 && !w.see[g].any(w.tiles.key(w.tiles.from + last[g]))) --last[g];
+            if (w.see[g].hi > 0 && ok) ok = wait_poll(ABAR(C::B_Q + g), (n_q >> g) & 1u, abort_flag);
+          }
+          for (int i = -1; i < count && ok; ++i) {
+            const bool more = i + 1 < count;
+            const int j = i >= 0 ? w.tiles.key(w.tiles.from + i) : 0, jn = more ? w.tiles.key(w.tiles.from + i + 1) : 0;
+            bool have_v = false, have_k = false;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              if (i >= 0 && w.see[g].any(j)) {  // O += P V
+                if (!have_v && !(ok = full(use + 2 * i + 1))) break;
+                have_v = true;
+                if (!(ok = wait_poll(ABAR(C::B_P + g), (n_p >> g) & 1u, abort_flag))) break;
+                n_p ^= 1u << g;
+                tc_fence_after();
+                const uint32_t v = stage(use + 2 * i + 1);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  umma_ts(tmem + C::O_COL + g * D, tmem + C::S_COL + g * 128 + c * 8, sdesc_sw128(v + c * 2048, 16384, 1024),
+                          idO, (((has_o >> g) & 1u) | uint32_t(c)) ? 1u : 0u);
+                has_o |= 1u << g;
+                if (i == last[g]) umma_commit(ABAR(C::B_O + g));
+              }
+              if (more && w.see[g].any(jn)) {  // S = Q K^T of the next tile
+                if (!have_k && !(ok = full(use + 2 * i + 2))) break;
+                have_k = true;
+                tc_fence_after();
+                const uint32_t q = base_u + C::OFF_Q + g * C::TILE, k = stage(use + 2 * i + 2);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                  const uint32_t off = (c >> 2) * 16384 + (c & 3) * 32;
+                  umma_ss(tmem + C::S_COL + g * 128, sdesc_sw128(q + off, 16, 1024), sdesc_sw128(k + off, 16, 1024), idS,
+                          c ? 1u : 0u);
+                }
+                umma_commit(ABAR(C::B_S + g));
+              }
+            }
+            if (!ok) break;
+            // a tile of the list is seen by one group at least, so its copies have been awaited
+            if (i >= 0) umma_commit(ABAR(C::B_EMPTY + (use + 2 * i + 1) % C::NS));
+            if (more) umma_commit(ABAR(C::B_EMPTY + (use + 2 * i + 2) % C::NS));
+            if (i + 2 >= count && !looked) {  // the run's last scores are issued: the queries may go
+#pragma unroll
+              for (int g = 0; g < 2; ++g)
+                if (w.see[g].hi > 0) {
+                  umma_commit(ABAR(C::B_QEMPTY + g));
+                  n_q ^= 1u << g;
+                }
+              next = attend_item<KV>(p, min(id + step, items - 1));  // while the products run
+              looked = true;
+            }
+          }
+          use += 2 * count;
         }
-        umma_commit(ABAR(C::B_S + g));
-      };
-      auto values = [&](int g, int i) {  // O += P V
-        const uint32_t v = stage(2 * i + 1);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          umma_ts(tmem + C::O_COL + g * D, tmem + C::S_COL + g * 128 + c * 8, sdesc_sw128(v + c * 2048, 16384, 1024), idO,
-                  (((has_o >> g) & 1u) | uint32_t(c)) ? 1u : 0u);
-        has_o |= 1u << g;
-      };
-      const int count = tiles.to - tiles.from;
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-        if (see[g].hi > 0 && ok) ok = wait_poll(ABAR(C::B_Q + g), 0, abort_flag);
-      for (int i = -1; i < count && ok; ++i) {
-        const bool more = i + 1 < count;
-        const int j = i >= 0 ? tiles.key(tiles.from + i) : 0, jn = more ? tiles.key(tiles.from + i + 1) : 0;
-        bool have_v = false, have_k = false;
+        if (!looked) next = attend_item<KV>(p, min(id + step, items - 1));
+        w = next;
+        id += step;
+      }
+      umma_commit(ABAR(C::B_END));
+      wait_drain(ABAR(C::B_END), 0);  // nothing of ours may run on after the CTA frees TMEM
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------- queries; paged: rows nobody may see, codes
+    bool ok = true;
+    int use = 0;
+    uint32_t n_q = 0, q_loaded = 0;  // bit g: phase of the queries, some were loaded
+    for (int id = blockIdx.x; id < items && ok; id += step) {
+      const AttendItem w = attend_item<KV>(p, id);
+      if (!w.real) continue;
+      const int count = w.tiles.to - w.tiles.from;
+      if (warp == 3) {
+        // the item's queries, once the last scores of the item before are done
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          if (i >= 0 && see[g].any(j)) {
-            if (!have_v && !(ok = full(2 * i + 1))) break;
-            have_v = true;
-            if (!(ok = wait_poll(ABAR(C::B_P + g), (n_p >> g) & 1u, abort_flag))) break;
-            n_p ^= 1u << g;
-            tc_fence_after();
-            values(g, i);
+          if (w.see[g].hi == 0) continue;
+          if (ok) ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_QEMPTY + g), ((n_q >> g) & 1u) ^ 1u, abort_flag));
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(ABAR(C::B_Q + g), p.rt.tokens * p.rt.heads * D * 2);
+#pragma unroll
+            for (int pn = 0; pn < D / 64; ++pn)
+              tma_load_3d(base_u + C::OFF_Q + g * C::TILE + pn * 16384, &tmQ, ABAR(C::B_Q + g), pn * 64, w.t0[g], w.head0);
           }
-          if (more && see[g].any(jn)) {
-            if (!have_k && !(ok = full(2 * i + 2))) break;
-            have_k = true;
-            tc_fence_after();
-            scores(g, i + 1);
+          if (ok) {
+            n_q ^= 1u << g;
+            q_loaded |= 1u << g;
           }
         }
         if (!ok) break;
-        // a tile of the list is seen by one group at least, so its copies have been awaited
-        if (i >= 0) umma_commit(ABAR(C::B_EMPTY + (2 * i + 1) % C::NS));
-        if (more) umma_commit(ABAR(C::B_EMPTY + (2 * i + 2) % C::NS));
       }
-      umma_commit(ABAR(C::B_O));
-      wait_drain(ABAR(C::B_O), 0);  // nothing of ours may run on after the CTA frees TMEM
-    }
-  } else if (warp < 4) {
-    // ------------------------------------------------------------- paged: rows nobody may see
-    if constexpr (KV == kKvPagedE4m3) {
-      // 16 codes per thread and step -> 32 bytes of the swizzled operand; rows that nobody may
-      // see become zero. The scales stay out: scores and weights take them exactly in fp32.
-      const int count = tiles.to - tiles.from, ct = threadIdx.x - 64;
-      constexpr int CH = D / 16;  // 16-code chunks of a row
-      for (int u = 0; u < 2 * count; ++u) {
-        const int sl = u % C::NL, s = u % C::NS, j0 = tiles.key(tiles.from + (u >> 1));
-        const uint32_t held = held_pages(p.pages, b, both, j0, lane);
-        bool ok = wait_bounded(ABAR(C::B_EMPTY + s), ((u / C::NS) & 1) ^ 1, abort_flag) &&
-                  wait_bounded(ABAR(C::B_LAND + sl), (u / C::NL) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) break;
+      if constexpr (KV == kKvPagedE4m3) {
+        // 16 codes per thread and step -> 32 bytes of the swizzled operand; rows that nobody may
+        // see become zero. The scales stay out: scores and weights take them exactly in fp32.
+        const int ct = threadIdx.x - 64;
+        constexpr int CH = D / 16;  // 16-code chunks of a row
+        for (int u = use; u < use + 2 * count; ++u) {
+          const int sl = u % C::NL, s = u % C::NS, j0 = w.tiles.key(w.tiles.from + ((u - use) >> 1));
+          const uint32_t held = held_pages(p.pages, w.b, w.both, j0, lane);
+          ok = wait_bounded(ABAR(C::B_EMPTY + s), ((u / C::NS) & 1) ^ 1, abort_flag) &&
+               wait_bounded(ABAR(C::B_LAND + sl), (u / C::NL) & 1, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
 #pragma unroll 4
-        for (int x = ct; x < 128 * CH; x += 64) {
-          const int r = x / CH, c = x % CH, j = j0 + r;
-          uint4 code = *reinterpret_cast<const uint4*>(base + C::OFF_CODES + sl * C::LAND + r * D + c * 16);
-          const bool in = ((held >> (r >> p.pages.log_page)) & 1u) && (j < both.sk || (j >= both.lo && j < both.hi));
-          if (!in) code = make_uint4(0, 0, 0, 0);
-          const uint4 lo = make_uint4(e4m3x2_to_bf16x2(code.x), e4m3x2_to_bf16x2(code.x >> 16),
-                                      e4m3x2_to_bf16x2(code.y), e4m3x2_to_bf16x2(code.y >> 16));
-          const uint4 hi = make_uint4(e4m3x2_to_bf16x2(code.z), e4m3x2_to_bf16x2(code.z >> 16),
-                                      e4m3x2_to_bf16x2(code.w), e4m3x2_to_bf16x2(code.w >> 16));
-          uint8_t* dst = base + C::OFF_RING + s * C::TILE + (c >> 2) * 16384 + r * 128;
-          const int c0 = (2 * c) & 7;
-          *reinterpret_cast<uint4*>(dst + ((c0 ^ (r & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = hi;
-        }
-        fence_proxy_async_smem();
-        warp_arrive(ABAR(C::B_FULL + s));
-        warp_arrive(ABAR(C::B_LEMPTY + sl));
-      }
-    } else if constexpr (KV == kKvPaged) {
-      if (warp == 2) {
-        const int count = tiles.to - tiles.from;
-        for (int u = 0; u < 2 * count; ++u) {
-          const int s = u % C::NS, j0 = tiles.key(tiles.from + (u >> 1));
-          if (!__all_sync(0xffffffffu, wait_bounded(ABAR(C::B_LAND + s), (u / C::NS) & 1, abort_flag))) break;
-          if (u & 1) {
-            const uint32_t held = held_pages(p.pages, b, both, j0, lane);
-            for (int r = lane; r < 128; r += 32) {
-              const int j = j0 + r;
-              const bool in = ((held >> (r >> p.pages.log_page)) & 1u) && (j < both.sk || (j >= both.lo && j < both.hi));
-              if (!in)
-                for (int pn = 0; pn < D / 64; ++pn)
-#pragma unroll
-                  for (int c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint4*>(base + C::OFF_RING + s * C::TILE + pn * 16384 + r * 128 + c * 16) =
-                        make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
+          for (int x = ct; x < 128 * CH; x += 64) {
+            const int r = x / CH, c = x % CH, j = j0 + r;
+            uint4 code = *reinterpret_cast<const uint4*>(base + C::OFF_CODES + sl * C::LAND + r * D + c * 16);
+            const bool in = ((held >> (r >> p.pages.log_page)) & 1u) && (j < w.both.sk || (j >= w.both.lo && j < w.both.hi));
+            if (!in) code = make_uint4(0, 0, 0, 0);
+            const uint4 lo = make_uint4(e4m3x2_to_bf16x2(code.x), e4m3x2_to_bf16x2(code.x >> 16),
+                                        e4m3x2_to_bf16x2(code.y), e4m3x2_to_bf16x2(code.y >> 16));
+            const uint4 hi = make_uint4(e4m3x2_to_bf16x2(code.z), e4m3x2_to_bf16x2(code.z >> 16),
+                                        e4m3x2_to_bf16x2(code.w), e4m3x2_to_bf16x2(code.w >> 16));
+            uint8_t* dst = base + C::OFF_RING + s * C::TILE + (c >> 2) * 16384 + r * 128;
+            const int c0 = (2 * c) & 7;
+            *reinterpret_cast<uint4*>(dst + ((c0 ^ (r & 7)) << 4)) = lo;
+            *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = hi;
           }
+          fence_proxy_async_smem();
           warp_arrive(ABAR(C::B_FULL + s));
+          warp_arrive(ABAR(C::B_LEMPTY + sl));
+        }
+      } else if constexpr (KV == kKvPaged) {
+        if (warp == 2) {
+          for (int u = use; u < use + 2 * count; ++u) {
+            const int s = u % C::NS, j0 = w.tiles.key(w.tiles.from + ((u - use) >> 1));
+            ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_LAND + s), (u / C::NS) & 1, abort_flag));
+            if (!ok) break;
+            // values of rows that the window's or the sequence's edge leaves out
+            const bool inner = j0 + 128 <= w.both.sk || (j0 >= w.both.lo && j0 + 128 <= w.both.hi);
+            const uint32_t held = (u - use) & 1 ? held_pages(p.pages, w.b, w.both, j0, lane) : 0u;
+            if (((u - use) & 1) && !(inner && held == (1u << (128 >> p.pages.log_page)) - 1u)) {
+              for (int r = lane; r < 128; r += 32) {
+                const int j = j0 + r;
+                const bool in = ((held >> (r >> p.pages.log_page)) & 1u) && (j < w.both.sk || (j >= w.both.lo && j < w.both.hi));
+                if (!in)
+                  for (int pn = 0; pn < D / 64; ++pn)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                      *reinterpret_cast<uint4*>(base + C::OFF_RING + s * C::TILE + pn * 16384 + r * 128 + c * 16) =
+                          make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+            }
+            warp_arrive(ABAR(C::B_FULL + s));
+          }
         }
       }
+      use += 2 * count;
     }
+    // no copy may still be in flight when the CTA exits
+    if (lane == 0)
+      for (int g = 0; g < 2; ++g)
+        if ((q_loaded >> g) & 1u) wait_drain(ABAR(C::B_Q + g), ((n_q >> g) & 1u) ^ 1u);
   } else {
     // ------------------------------------------------------------- softmax
     const int g = (warp - 4) >> 2;
-    const Sight mine = g ? see[1] : see[0];
-    const int r = row0 + 128 * g + (threadIdx.x & 127);
+    const int my_head = int(threadIdx.x & 127) / p.rt.tokens, my_token = int(threadIdx.x & 127) - my_head * p.rt.tokens;
     const uint32_t lrow = uint32_t((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + lrow + C::S_COL + g * 128, o_addr = tmem + lrow + C::O_COL + g * D;
-    const bool real = r < rows;
-    const int t = real ? r / G : 0, head = hk * G + (real ? r % G : 0);
-    const size_t row = (size_t(b) * p.Hq + head) * p.N + t;
-    const int pos = n - nq + t;
-    bool ok = true;
-    if (mine.hi > 0) {
-      // this row's query into the 128-byte swizzled operand
-      const uint4* src = reinterpret_cast<const uint4*>(p.Q + row * D);
-      const int rt = threadIdx.x & 127;
-      uint8_t* dst = base + C::OFF_Q + g * C::TILE + rt * 128;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c)
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (rt & 7)) << 4)) =
-            real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
-      warp_arrive(ABAR(C::B_Q + g));
-    }
     const float sl2 = p.scale * 1.4426950408889634f;
-    // the keys this row sees: up to z, and from a on or below the sinks' end
-    const int z = max(-1, min(n - 1, pos + p.win.right)), a = max(0, pos - p.win.left);
-    // 8 bits: a warp keeps its tile's scales in shared memory, the next tile's in registers
-    float4 next_k, next_v;
     float* scales = reinterpret_cast<float*>(base + C::OFF_SCALE) + (C::CODES ? (warp - 4) * 256 : 0);
-    auto fetch_scales = [&](int i) {
-      next_k = next_v = make_float4(0.f, 0.f, 0.f, 0.f);  // keys that nobody may see weigh nothing
-      while (i < tiles.to && !mine.any(tiles.key(i))) ++i;
-      if (i >= tiles.to) return;
-      const int j = tiles.key(i) + 4 * lane, page = p.pages.table[size_t(b) * p.pages.max_pages + min(j, n - 1) / (1 << p.pages.log_page)];
-      const bool in = mine.any(j, 4) && page >= 0 && page < p.pages.num_pages;
-      if (!in) return;
-      const size_t at = ((size_t(page) * p.Hkv + hk) << p.pages.log_page) + (j & ((1 << p.pages.log_page) - 1));
-      next_k = __ldg(reinterpret_cast<const float4*>(p.pages.ks + at));
-      next_v = __ldg(reinterpret_cast<const float4*>(p.pages.vs + at));
-      float* f = reinterpret_cast<float*>(&next_v);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (!(j + k < mine.sk || (j + k >= mine.lo && j + k < mine.hi))) f[k] = 0.f;
-    };
-    if constexpr (C::CODES) fetch_scales(tiles.from);
-    float m = -INFINITY, l = 0.f;
-    uint32_t phase = 0, done = 0;
-    for (int i = tiles.from; i < tiles.to; ++i) {
-      const int j0 = tiles.key(i);
-      if (!mine.any(j0)) continue;
-      uint32_t held = 0xffu;
-      if constexpr (KV != kKvPlain) held = held_pages(p.pages, b, mine, j0, lane);
-      const bool whole = j0 + 127 <= mine.p0 + p.win.right && j0 + 128 <= n &&
-                         (j0 >= mine.p1 - p.win.left || j0 + 128 <= p.win.sinks) &&
-                         (KV == kKvPlain || held == (1u << (128 >> p.pages.log_page)) - 1u);
-      if constexpr (C::CODES) {
-        __syncwarp();  // the previous tile's scales have been read
-        reinterpret_cast<float4*>(scales)[lane] = next_k;
-        reinterpret_cast<float4*>(scales + 128)[lane] = next_v;
-        __syncwarp();
-        fetch_scales(i + 1);
-        __syncwarp();
-      }
-      ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_S + g), phase, abort_flag));
-      if (!ok) break;
-      phase ^= 1u;
-      tc_fence_after();
-      uint32_t sc[128];
-#pragma unroll
-      for (int ch = 0; ch < 8; ++ch) tmem_ld16(s_addr + ch * 16, *reinterpret_cast<uint32_t(*)[16]>(&sc[ch * 16]));
-#pragma unroll
-      for (int ch = 0; ch < 8; ++ch) tmem_wait_ld(*reinterpret_cast<uint32_t(*)[16]>(&sc[ch * 16]));
-      if constexpr (C::CODES) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float4 f = reinterpret_cast<const float4*>(scales)[k];
-          sc[4 * k] = __float_as_uint(__uint_as_float(sc[4 * k]) * f.x);
-          sc[4 * k + 1] = __float_as_uint(__uint_as_float(sc[4 * k + 1]) * f.y);
-          sc[4 * k + 2] = __float_as_uint(__uint_as_float(sc[4 * k + 2]) * f.z);
-          sc[4 * k + 3] = __float_as_uint(__uint_as_float(sc[4 * k + 3]) * f.w);
-        }
-      }
-      if (!whole) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t bits = ones_below(z - j0 + 1 - 32 * w) &
-                          (~ones_below(a - j0 - 32 * w) | ones_below(p.win.sinks - j0 - 32 * w));
-          if constexpr (KV != kKvPlain) {
-            // 32 keys are one page of 32, a part of a larger one, or two of 16
-            if (p.pages.log_page >= 5) bits = ((held >> ((32 * w) >> p.pages.log_page)) & 1u) ? bits : 0u;
-            else bits &= ((held >> (2 * w)) & 1u ? 0xffffu : 0u) | ((held >> (2 * w + 1)) & 1u ? 0xffff0000u : 0u);
-          }
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (!((bits >> k) & 1u)) sc[32 * w + k] = __float_as_uint(-INFINITY);
-        }
-      }
-      float mxp[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mxp[k] = __uint_as_float(sc[k]);
-#pragma unroll
-      for (int k = 8; k < 128; ++k) mxp[k & 7] = fmaxf(mxp[k & 7], __uint_as_float(sc[k]));
-      const float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
-                             fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7]))) * sl2;
-      const bool grow = mx > m + 8.f;
-      const bool move = grow && m != -INFINITY;
-      if (__any_sync(0xffffffffu, move)) {  // S(i) is behind every earlier product of the group
-        const float f = move ? ex2(m - mx) : 1.f;
-        rescale_row<D>(o_addr, f);
-        l *= f;
-      }
-      if (grow) m = mx;
-      const float negm = m == -INFINITY ? 0.f : -m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float e0 = ex2(fmaf(__uint_as_float(sc[ch * 32 + 2 * k]), sl2, negm));
-          const float e1 = ex2(fmaf(__uint_as_float(sc[ch * 32 + 2 * k + 1]), sl2, negm));
-          sum[k & 3] += e0 + e1;
-          if constexpr (C::CODES) {  // the value's scale may be NaN, or the weight huge beside it
-            const float2 f = reinterpret_cast<const float2*>(scales + 128)[ch * 16 + k];
-            pk[k] = pack_bf16x2(e0 * f.x, e1 * f.y);
-          } else {
-            pk[k] = pack_bf16x2_int(e0, e1);
-          }
-        }
-        tmem_st16(s_addr + ch * 16, pk);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      warp_arrive(ABAR(C::B_P + g));
-      done = 1;
-    }
-    ok = __all_sync(0xffffffffu, ok && wait_bounded(ABAR(C::B_O), 0, abort_flag));
-    tc_fence_after();
-    const float inv = l != 0.f ? 1.f / l : 0.f;  // l is NaN if a score was
-    const bool split_out = p.splits > 1;
-    const size_t at = size_t(split) * size_t(p.B) * p.Hq * p.N + row;
-#pragma unroll 1
-    for (int ch = 0; ch < D / 16; ++ch) {
-      __syncwarp();
-      uint32_t o[16];
-      if (done) {
-        tmem_ld16(o_addr + ch * 16, o);
-        tmem_wait_ld(o);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = 0u;
-      }
-      if (!real || !ok) continue;
-      if (split_out) {
+    bool ok = true;
+    uint32_t n_s = 0, n_o = 0;
+    for (int id = blockIdx.x; id < items && ok; id += step) {
+      const AttendItem w = attend_item<KV>(p, id);
+      if (!w.real) continue;
+      const Sight mine = g ? w.see[1] : w.see[0];
+      const int t0 = g ? w.t0[1] : w.t0[0];
+      const bool real = my_head < w.heads && t0 + my_token < w.nq;
+      const int t = t0 + (real ? my_token : 0);
+      const size_t row = size_t(w.head0 + (real ? my_head : 0)) * p.N + t;
+      const int pos = w.n - w.nq + t;
+      // the keys this row sees: up to z, and from a on or below the sinks' end
+      const int z = max(-1, min(w.n - 1, pos + p.win.right)), a = max(0, pos - p.win.left);
+      // 8 bits: a warp keeps its tile's scales in shared memory, the next tile's in registers
+      float4 next_k, next_v;
+      auto fetch_scales = [&](int i) {
+        next_k = next_v = make_float4(0.f, 0.f, 0.f, 0.f);  // keys that nobody may see weigh nothing
+        while (i < w.tiles.to && !mine.any(w.tiles.key(i))) ++i;
+        if (i >= w.tiles.to) return;
+        const int j = w.tiles.key(i) + 4 * lane;
+        const int page = p.pages.table[size_t(w.b) * p.pages.max_pages + (min(j, w.n - 1) >> p.pages.log_page)];
+        const bool in = mine.any(j, 4) && page >= 0 && page < p.pages.num_pages;
+        if (!in) return;
+        const size_t at = ((size_t(page) * p.Hkv + w.hk) << p.pages.log_page) + (j & ((1 << p.pages.log_page) - 1));
+        next_k = __ldg(reinterpret_cast<const float4*>(p.pages.ks + at));
+        next_v = __ldg(reinterpret_cast<const float4*>(p.pages.vs + at));
+        float* f = reinterpret_cast<float*>(&next_v);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          reinterpret_cast<float4*>(p.part + at * D + ch * 16)[k] =
-              make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
-                          __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
-      } else {
-        uint32_t w[8];
+          if (!(j + k < mine.sk || (j + k >= mine.lo && j + k < mine.hi))) f[k] = 0.f;
+      };
+      if constexpr (C::CODES) fetch_scales(w.tiles.from);
+      float m = -INFINITY, l = 0.f;
+      uint32_t done = 0;
+      for (int i = w.tiles.from; i < w.tiles.to; ++i) {
+        const int j0 = w.tiles.key(i);
+        if (!mine.any(j0)) continue;
+        uint32_t held = 0xffu;
+        if constexpr (KV != kKvPlain) held = held_pages(p.pages, w.b, mine, j0, lane);
+        const bool whole = j0 + 127 <= mine.p0 + p.win.right && j0 + 128 <= w.n &&
+                           (j0 >= mine.p1 - p.win.left || j0 + 128 <= p.win.sinks) &&
+                           (KV == kKvPlain || held == (1u << (128 >> p.pages.log_page)) - 1u);
+        if constexpr (C::CODES) {
+          __syncwarp();  // the previous tile's scales have been read
+          reinterpret_cast<float4*>(scales)[lane] = next_k;
+          reinterpret_cast<float4*>(scales + 128)[lane] = next_v;
+          __syncwarp();
+          fetch_scales(i + 1);
+          __syncwarp();
+        }
+        ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_S + g), n_s, abort_flag));
+        if (!ok) break;
+        n_s ^= 1u;
+        tc_fence_after();
+        uint32_t sc[128];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          w[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-        uint4* dst = reinterpret_cast<uint4*>(p.O + row * D + ch * 16);
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int ch = 0; ch < 8; ++ch) tmem_ld16(s_addr + ch * 16, *reinterpret_cast<uint32_t(*)[16]>(&sc[ch * 16]));
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) tmem_wait_ld(*reinterpret_cast<uint32_t(*)[16]>(&sc[ch * 16]));
+        if constexpr (C::CODES) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float4 f = reinterpret_cast<const float4*>(scales)[k];
+            sc[4 * k] = __float_as_uint(__uint_as_float(sc[4 * k]) * f.x);
+            sc[4 * k + 1] = __float_as_uint(__uint_as_float(sc[4 * k + 1]) * f.y);
+            sc[4 * k + 2] = __float_as_uint(__uint_as_float(sc[4 * k + 2]) * f.z);
+            sc[4 * k + 3] = __float_as_uint(__uint_as_float(sc[4 * k + 3]) * f.w);
+          }
+        }
+        if (!whole) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t bits = ones_below(z - j0 + 1 - 32 * x) &
+                            (~ones_below(a - j0 - 32 * x) | ones_below(p.win.sinks - j0 - 32 * x));
+            if constexpr (KV != kKvPlain) {
+              // 32 keys are one page of 32, a part of a larger one, or two of 16
+              if (p.pages.log_page >= 5) bits = ((held >> ((32 * x) >> p.pages.log_page)) & 1u) ? bits : 0u;
+              else bits &= ((held >> (2 * x)) & 1u ? 0xffffu : 0u) | ((held >> (2 * x + 1)) & 1u ? 0xffff0000u : 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!((bits >> k) & 1u)) sc[32 * x + k] = __float_as_uint(-INFINITY);
+          }
+        }
+        float mxp[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mxp[k] = __uint_as_float(sc[k]);
+#pragma unroll
+        for (int k = 8; k < 128; ++k) mxp[k & 7] = fmaxf(mxp[k & 7], __uint_as_float(sc[k]));
+        const float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
+                               fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7]))) * sl2;
+        const bool grow = mx > m + 8.f;
+        const bool move = grow && m != -INFINITY;
+        if (__any_sync(0xffffffffu, move)) {  // S(i) is behind every earlier product of the group
+          const float f = move ? ex2(m - mx) : 1.f;
+          rescale_row<D>(o_addr, f);
+          l *= f;
+        }
+        if (grow) m = mx;
+        const float negm = m == -INFINITY ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float e0 = ex2(fmaf(__uint_as_float(sc[ch * 32 + 2 * k]), sl2, negm));
+            const float e1 = ex2(fmaf(__uint_as_float(sc[ch * 32 + 2 * k + 1]), sl2, negm));
+            sum[k & 3] += e0 + e1;
+            if constexpr (C::CODES) {  // the value's scale may be NaN, or the weight huge beside it
+              const float2 f = reinterpret_cast<const float2*>(scales + 128)[ch * 16 + k];
+              pk[k] = pack_bf16x2(e0 * f.x, e1 * f.y);
+            } else {
+              pk[k] = pack_bf16x2_int(e0, e1);
+            }
+          }
+          tmem_st16(s_addr + ch * 16, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(ABAR(C::B_P + g));
+        done = 1;
       }
+      if (ok && done) {
+        ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_O + g), n_o, abort_flag));
+        n_o ^= 1u;
+      }
+      if (!ok) break;
+      tc_fence_after();
+      const float inv = l != 0.f ? 1.f / l : 0.f;  // l is NaN if a score was
+      const bool split_out = p.splits > 1;
+      const size_t at = size_t(w.split) * size_t(p.B) * p.Hq * p.N + row;
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        __syncwarp();
+        uint32_t o[2][16];
+        if (done) {
+          tmem_ld16(o_addr + ch * 32, o[0]);
+          tmem_ld16(o_addr + ch * 32 + 16, o[1]);
+          tmem_wait_ld(o[0]);
+          tmem_wait_ld(o[1]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[0][k] = o[1][k] = 0u;
+        }
+        if (!real) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (split_out) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              reinterpret_cast<float4*>(p.part + at * D + ch * 32 + h * 16)[k] =
+                  make_float4(__uint_as_float(o[h][4 * k]) * inv, __uint_as_float(o[h][4 * k + 1]) * inv,
+                              __uint_as_float(o[h][4 * k + 2]) * inv, __uint_as_float(o[h][4 * k + 3]) * inv);
+          } else {
+            uint32_t x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              x[k] = pack_bf16x2(__uint_as_float(o[h][2 * k]) * inv, __uint_as_float(o[h][2 * k + 1]) * inv);
+            uint4* dst = reinterpret_cast<uint4*>(p.O + row * D + ch * 32 + h * 16);
+            dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+            dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+          }
+        }
+      }
+      __syncwarp();
+      if (real) {
+        const float lg = l != 0.f ? m + __log2f(l) : -INFINITY;
+        if (split_out) p.part_lse[at] = lg;
+        else if (p.lse) p.lse[row] = lg * 0.6931471805599453f;
+      }
+      tc_fence_before();
     }
-    if (real && ok) {
-      const float lg = l != 0.f ? m + __log2f(l) : -INFINITY;
-      if (split_out) p.part_lse[at] = lg;
-      else if (p.lse) p.lse[row] = lg * 0.6931471805599453f;
-    }
-    tc_fence_before();
   }
   __syncthreads();
   if (warp == 2) {
