@@ -136,44 +136,51 @@ attend_dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         for (int u = use > C::NS ? use - C::NS : 0; u < use; ++u) wait_drain(ABAR(C::B_FULL + u % C::NS), (u / C::NS) & 1);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16(128, 128, false), idQ = idesc_bf16(128, D, true);
-      auto stage = [&](int use) { return base_u + C::OFF_RING + (use % C::NS) * C::TILE; };
-      auto full = [&](int use) { return wait_poll(ABAR(C::B_FULL + use % C::NS), (use / C::NS) & 1, abort_flag); };
-      auto rows_by = [&](uint32_t a, uint32_t t, uint32_t col) {  // A [128 rows][D] times the tile, transposed
+    constexpr uint32_t idS = idesc_bf16(128, 128, false), idQ = idesc_bf16(128, D, true);
+    const bool lead = elect();
+    auto stage = [&](int use) { return base_u + C::OFF_RING + (use % C::NS) * C::TILE; };
+    auto full = [&](int use) { return wait_warp(ABAR(C::B_FULL + use % C::NS), (use / C::NS) & 1, abort_flag); };
+    auto rows_by = [&](uint32_t a, uint32_t t, uint32_t col) {  // A [128 rows][D] times the tile, transposed
+      const uint64_t da = operand(a, 16), dt = operand(t, 16);
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint32_t off = (c >> 2) * 16384 + (c & 3) * 32;
-          umma_ss(tmem + col, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(t + off, 16, 1024), idS, c ? 1u : 0u);
-        }
-      };
-      bool ok = wait_poll(ABAR(C::B_Q), 0, abort_flag);
-      for (int i = -1; i < count && ok; ++i) {
-        if (i + 1 < count) {
-          if (!(ok = full(2 * i + 2))) break;
-          tc_fence_after();
-          rows_by(base_u + C::OFF_Q, stage(2 * i + 2), C::S_COL + ((i + 1) & 1) * 128);
-          if (i >= 0 && !(ok = wait_poll(ABAR(C::B_R), i & 1, abort_flag))) break;
-          if (!(ok = full(2 * i + 3))) break;
-          tc_fence_after();
+      for (int c = 0; c < D / 16; ++c) {
+        const uint32_t off = ((c >> 2) * 16384 + (c & 3) * 32) >> 4;
+        umma_ss(tmem + col, da + off, dt + off, idS, c ? 1u : 0u);
+      }
+    };
+    bool ok = wait_warp(ABAR(C::B_Q), 0, abort_flag);
+    for (int i = -1; i < count && ok; ++i) {
+      if (i + 1 < count) {
+        if (!(ok = full(2 * i + 2))) break;
+        tc_fence_after();
+        if (lead) rows_by(base_u + C::OFF_Q, stage(2 * i + 2), C::S_COL + ((i + 1) & 1) * 128);
+        if (i >= 0 && !(ok = wait_warp(ABAR(C::B_R), i & 1, abort_flag))) break;
+        if (!(ok = full(2 * i + 3))) break;
+        tc_fence_after();
+        if (lead) {
           rows_by(base_u + C::OFF_DO, stage(2 * i + 3), C::DP_COL);
           umma_commit(ABAR(C::B_SD));
           umma_commit(ABAR(C::B_EMPTY + (2 * i + 3) % C::NS));
         }
-        if (i < 0) continue;
-        if (!(ok = wait_poll(ABAR(C::B_DS), i & 1, abort_flag))) break;
-        tc_fence_after();
-        const uint32_t k = stage(2 * i), ds = tmem + C::S_COL + (i & 1) * 128;
+      }
+      if (i < 0) continue;
+      if (!(ok = wait_warp(ABAR(C::B_DS), i & 1, abort_flag))) break;
+      tc_fence_after();
+      if (lead) {
+        const uint64_t k = operand(stage(2 * i), 16384);
+        const uint32_t ds = tmem + C::S_COL + (i & 1) * 128;
         // keys [16c, 16c + 16): the thread of half c / 4 packed them at the start of its columns
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          umma_ts(tmem + C::DQ_COL, ds + (c >> 2) * 64 + (c & 3) * 8, sdesc_sw128(k + c * 2048, 16384, 1024), idQ,
-                  (i | c) ? 1u : 0u);
+          umma_ts(tmem + C::DQ_COL, ds + (c >> 2) * 64 + (c & 3) * 8, k + c * (2048 >> 4), idQ, (i | c) ? 1u : 0u);
         umma_commit(ABAR(C::B_EMPTY + (2 * i) % C::NS));
       }
+    }
+    if (lead) {
       umma_commit(ABAR(C::B_O));
       wait_drain(ABAR(C::B_O), 0);
     }
+    __syncwarp();
   } else if (warp >= 4) {
     // two threads per row: half hf has keys [64 hf, 64 hf + 64) of a tile, and D/2 dimensions
     const int hf = (warp - 4) >> 2, rt = threadIdx.x & 127;
@@ -452,43 +459,50 @@ attend_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16(128, 64, false), idG = idesc_bf16(128, D, true);
-      const int count = to - from;
-      auto stage = [&](int i) { return base_u + C::OFF_RING + (i % C::NS) * 2 * C::QTILE; };
-      auto scores = [&](int i) -> bool {  // S^T = K Q^T, dP^T = V dO^T of the run's i-th tile
-        if (!wait_poll(ABAR(C::B_FULL + i % C::NS), (i / C::NS) & 1, abort_flag)) return false;
-        tc_fence_after();
-        const uint32_t q = stage(i);
+    constexpr uint32_t idS = idesc_bf16(128, 64, false), idG = idesc_bf16(128, D, true);
+    const bool lead = elect();
+    const int count = to - from;
+    auto stage = [&](int i) { return base_u + C::OFF_RING + (i % C::NS) * 2 * C::QTILE; };
+    auto scores = [&](int i) -> bool {  // S^T = K Q^T, dP^T = V dO^T of the run's i-th tile
+      if (!wait_warp(ABAR(C::B_FULL + i % C::NS), (i / C::NS) & 1, abort_flag)) return false;
+      tc_fence_after();
+      if (lead) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+        for (int w = 0; w < 2; ++w) {
+          const uint64_t a = operand(base_u + (w ? C::OFF_V : C::OFF_K), 16), q = operand(stage(i) + w * C::QTILE, 16);
 #pragma unroll
           for (int c = 0; c < D / 16; ++c)
-            umma_ss(tmem + (w ? C::DP_COL : C::S_COL) + (i & 1) * 64,
-                    sdesc_sw128(base_u + (w ? C::OFF_V : C::OFF_K) + (c >> 2) * 16384 + (c & 3) * 32, 16, 1024),
-                    sdesc_sw128(q + w * C::QTILE + (c >> 2) * 8192 + (c & 3) * 32, 16, 1024), idS, c ? 1u : 0u);
+            umma_ss(tmem + (w ? C::DP_COL : C::S_COL) + (i & 1) * 64, a + (((c >> 2) * 16384 + (c & 3) * 32) >> 4),
+                    q + (((c >> 2) * 8192 + (c & 3) * 32) >> 4), idS, c ? 1u : 0u);
+        }
         umma_commit(ABAR(C::B_SD + (i & 1)));
-        return true;
-      };
-      bool ok = wait_poll(ABAR(C::B_KV), 0, abort_flag);
-      if (ok) ok = scores(0);
-      if (ok && count > 1) ok = scores(1);
-      for (int i = 0; i < count && ok; ++i) {
-        if (!(ok = wait_poll(ABAR(C::B_PD + (i & 1)), (i >> 1) & 1, abort_flag))) break;
-        tc_fence_after();
-        const uint32_t q = stage(i);
+      }
+      return true;
+    };
+    bool ok = wait_warp(ABAR(C::B_KV), 0, abort_flag);
+    if (ok) ok = scores(0);
+    if (ok && count > 1) ok = scores(1);
+    for (int i = 0; i < count && ok; ++i) {
+      if (!(ok = wait_warp(ABAR(C::B_PD + (i & 1)), (i >> 1) & 1, abort_flag))) break;
+      tc_fence_after();
+      if (lead) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+        for (int w = 0; w < 2; ++w) {
+          const uint64_t q = operand(stage(i) + (w ? 0 : C::QTILE), 8192);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             umma_ts(tmem + (w ? C::DK_COL : C::DV_COL), tmem + (w ? C::DP_COL : C::S_COL) + (i & 1) * 64 + c * 8,
-                    sdesc_sw128(q + (w ? 0 : C::QTILE) + c * 2048, 8192, 1024), idG, (i | c) ? 1u : 0u);
+                    q + c * (2048 >> 4), idG, (i | c) ? 1u : 0u);
+        }
         umma_commit(ABAR(C::B_EMPTY + i % C::NS));
-        if (i + 2 < count) ok = scores(i + 2);
       }
+      if (i + 2 < count) ok = scores(i + 2);
+    }
+    if (lead) {
       umma_commit(ABAR(C::B_O));
       wait_drain(ABAR(C::B_O), 0);
     }
+    __syncwarp();
   } else if (warp == 2) {
     // each tile's row statistics; rows behind the last one weigh nothing
     for (int i = from, use = 0; i < to; ++i, ++use) {

@@ -10,7 +10,7 @@
 // window's); a group skips the ones that none of its rows sees. Warp roles:
 //   warp 0       producer: K and V tiles by TMA (a page at a time in a paged cache) into a ring,
 //                running ahead into the next item;
-//   warp 1       one thread issues every tcgen05.mma: per tile and group S = Q K^T (SS), then
+//   warp 1       issues every tcgen05.mma: per tile and group S = Q K^T (SS), then
 //                O += P V (TS, P from tensor memory);
 //   warp 3       loads the next item's queries once the last scores of this one are done;
 //   warp 2       paged caches: clears the rows of a V tile that no row may see (unwritten rows
@@ -20,7 +20,7 @@
 // S) and O of either group (D columns each).
 //
 // The two groups alternate on the tensor core: while one group's exponentials run, the other's
-// P V and next Q K^T do. Products are issued by one thread and execute in order, so S of tile
+// P V and next Q K^T do. Products are issued by one lane and execute in order, so S of tile
 // i + 1 may overwrite P of tile i behind the P V that reads it, and a group that sees its S(i + 1)
 // (one commit) knows its O holds the products up to tile i: O is rescaled without a further
 // wait. The accumulator is rescaled only when the maximum grows by more than 2^8.
@@ -136,6 +136,55 @@ __device__ __forceinline__ uint32_t held_pages(const Pages& g, int b, const Sigh
     ok = a.any(j, 1 << g.log_page) && page_of(g, b, j) >= 0;
   }
   return __ballot_sync(0xffffffffu, ok);
+}
+
+// A 128-byte swizzled operand at `saddr` as its descriptor; a product's step adds its offset in
+// 16-byte units to the low word. All lanes of the issuing warp run the loop and hold the same
+// values, so that they stay in uniform registers; one lane issues. (With the loop in one lane's
+// branch each product took about 95 cycles to issue against 64 to execute.)
+__device__ __forceinline__ uint64_t operand(uint32_t saddr, uint32_t lbo) { return tc::sdesc_sw128(saddr, lbo, 1024); }
+__device__ __forceinline__ bool elect() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+// wait of a whole warp that issues products
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, tc::wait_poll(bar, parity, abort_flag));
+}
+
+// 32 fp32 columns of a warp's 32 rows (lane = row) as bf16 at dst[row] + 0 .. 31. The lanes of a
+// quad exchange 16-byte pieces so that each store covers 64 contiguous bytes of eight rows, not 16
+// of 32 (5000 cycles for a tile of 128 x 128 at one row per lane). `at`: element offset of this
+// lane's row, < 0 if it is not written.
+__device__ __forceinline__ void store_rows32(bf16* dst, int64_t at, const uint32_t (&x)[2][16], float scale) {
+  uint32_t c[4][4];
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    c[k >> 2][k & 3] = pack_bf16x2(__uint_as_float(x[k >> 3][(2 * k) & 15]) * scale, __uint_as_float(x[k >> 3][(2 * k + 1) & 15]) * scale);
+  const int q = threadIdx.x & 3;
+#pragma unroll
+  for (int d = 1; d <= 2; ++d)  // 4 x 4 transposition of pieces: partners at distance d
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int a = d == 1 ? 2 * e : e, b = a + d;
+      const bool high = (q & d) != 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? c[a][k] : c[b][k], d);
+        if (high) c[a][k] = got;
+        else c[b][k] = got;
+      }
+    }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // piece q of the quad's row j
+    const int64_t to = __shfl_sync(0xffffffffu, at, (threadIdx.x & 28) + j);
+    if (to >= 0) *reinterpret_cast<uint4*>(dst + to + q * 8) = make_uint4(c[j][0], c[j][1], c[j][2], c[j][3]);
+  }
 }
 
 // One piece of work: two tiles of a key head's rows over one run of their key tiles.
@@ -287,86 +336,93 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- products
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16(128, 128, false), idO = idesc_bf16(128, D, true);
-      bool ok = true;
-      uint32_t n_p = 0, n_q = 0;  // bit g: phase of P, of the queries
-      int use = 0;                // stage uses of the items before
-      auto stage = [&](int u) { return base_u + C::OFF_RING + (u % C::NS) * C::TILE; };
-      auto full = [&](int u) { return wait_poll(ABAR(C::B_FULL + u % C::NS), (u / C::NS) & 1, abort_flag); };
-      int id = blockIdx.x;
-      AttendItem w = attend_item<KV>(p, id);
-      while (id < items && ok) {
-        const int count = w.tiles.to - w.tiles.from;
-        uint32_t has_o = 0;  // bit g: O holds a product of this item
-        AttendItem next;
-        bool looked = false;
-        if (w.real) {
-          int last[2];  // a group's last tile of the run
+    constexpr uint32_t idS = idesc_bf16(128, 128, false), idO = idesc_bf16(128, D, true);
+    const bool lead = elect();
+    bool ok = true;
+    uint32_t n_p = 0, n_q = 0;  // bit g: phase of P, of the queries
+    int use = 0;                // stage uses of the items before
+    auto stage = [&](int u) { return base_u + C::OFF_RING + (u % C::NS) * C::TILE; };
+    auto full = [&](int u) { return wait_warp(ABAR(C::B_FULL + u % C::NS), (u / C::NS) & 1, abort_flag); };
+    int id = blockIdx.x;
+    AttendItem w = attend_item<KV>(p, id);
+    while (id < items && ok) {
+      const int count = w.tiles.to - w.tiles.from;
+      uint32_t has_o = 0;  // bit g: O holds a product of this item
+      AttendItem next;
+      bool looked = false;
+      if (w.real) {
+        int last[2];  // a group's last tile of the run
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          last[g] = count - 1;
+          while (last[g] >= 0 && !w.see[g].any(w.tiles.key(w.tiles.from + last[g]))) --last[g];
+          if (w.see[g].hi > 0 && ok) ok = wait_warp(ABAR(C::B_Q + g), (n_q >> g) & 1u, abort_flag);
+        }
+        for (int i = -1; i < count && ok; ++i) {
+          const bool more = i + 1 < count;
+          const int j = i >= 0 ? w.tiles.key(w.tiles.from + i) : 0, jn = more ? w.tiles.key(w.tiles.from + i + 1) : 0;
+          const uint64_t v = operand(stage(use + 2 * i + 1), 16384), k = operand(stage(use + 2 * i + 2), 16);
+          bool have_v = false, have_k = false;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            last[g] = count - 1;
-            while (last[g] >= 0 && !w.see[g].any(w.tiles.key(w.tiles.from + last[g]))) --last[g];
-            if (w.see[g].hi > 0 && ok) ok = wait_poll(ABAR(C::B_Q + g), (n_q >> g) & 1u, abort_flag);
-          }
-          for (int i = -1; i < count && ok; ++i) {
-            const bool more = i + 1 < count;
-            const int j = i >= 0 ? w.tiles.key(w.tiles.from + i) : 0, jn = more ? w.tiles.key(w.tiles.from + i + 1) : 0;
-            bool have_v = false, have_k = false;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              if (i >= 0 && w.see[g].any(j)) {  // O += P V
-                if (!have_v && !(ok = full(use + 2 * i + 1))) break;
-                have_v = true;
-                if (!(ok = wait_poll(ABAR(C::B_P + g), (n_p >> g) & 1u, abort_flag))) break;
-                n_p ^= 1u << g;
-                tc_fence_after();
-                const uint32_t v = stage(use + 2 * i + 1);
+            if (i >= 0 && w.see[g].any(j)) {  // O += P V
+              if (!have_v && !(ok = full(use + 2 * i + 1))) break;
+              have_v = true;
+              if (!(ok = wait_warp(ABAR(C::B_P + g), (n_p >> g) & 1u, abort_flag))) break;
+              n_p ^= 1u << g;
+              tc_fence_after();
+              if (lead) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                  umma_ts(tmem + C::O_COL + g * D, tmem + C::S_COL + g * 128 + c * 8, sdesc_sw128(v + c * 2048, 16384, 1024),
-                          idO, (((has_o >> g) & 1u) | uint32_t(c)) ? 1u : 0u);
-                has_o |= 1u << g;
+                  umma_ts(tmem + C::O_COL + g * D, tmem + C::S_COL + g * 128 + c * 8, v + c * (2048 >> 4), idO,
+                          (((has_o >> g) & 1u) | uint32_t(c)) ? 1u : 0u);
                 if (i == last[g]) umma_commit(ABAR(C::B_O + g));
               }
-              if (more && w.see[g].any(jn)) {  // S = Q K^T of the next tile
-                if (!have_k && !(ok = full(use + 2 * i + 2))) break;
-                have_k = true;
-                tc_fence_after();
-                const uint32_t q = base_u + C::OFF_Q + g * C::TILE, k = stage(use + 2 * i + 2);
+              has_o |= 1u << g;
+            }
+            if (more && w.see[g].any(jn)) {  // S = Q K^T of the next tile
+              if (!have_k && !(ok = full(use + 2 * i + 2))) break;
+              have_k = true;
+              tc_fence_after();
+              if (lead) {
+                const uint64_t q = operand(base_u + C::OFF_Q + g * C::TILE, 16);
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
-                  const uint32_t off = (c >> 2) * 16384 + (c & 3) * 32;
-                  umma_ss(tmem + C::S_COL + g * 128, sdesc_sw128(q + off, 16, 1024), sdesc_sw128(k + off, 16, 1024), idS,
-                          c ? 1u : 0u);
+                  const uint32_t off = ((c >> 2) * 16384 + (c & 3) * 32) >> 4;
+                  umma_ss(tmem + C::S_COL + g * 128, q + off, k + off, idS, c ? 1u : 0u);
                 }
                 umma_commit(ABAR(C::B_S + g));
               }
             }
-            if (!ok) break;
-            // a tile of the list is seen by one group at least, so its copies have been awaited
+          }
+          if (!ok) break;
+          // a tile of the list is seen by one group at least, so its copies have been awaited
+          if (lead) {
             if (i >= 0) umma_commit(ABAR(C::B_EMPTY + (use + 2 * i + 1) % C::NS));
             if (more) umma_commit(ABAR(C::B_EMPTY + (use + 2 * i + 2) % C::NS));
-            if (i + 2 >= count && !looked) {  // the run's last scores are issued: the queries may go
-#pragma unroll
-              for (int g = 0; g < 2; ++g)
-                if (w.see[g].hi > 0) {
-                  umma_commit(ABAR(C::B_QEMPTY + g));
-                  n_q ^= 1u << g;
-                }
-              next = attend_item<KV>(p, min(id + step, items - 1));  // while the products run
-              looked = true;
-            }
           }
-          use += 2 * count;
+          if (i + 2 >= count && !looked) {  // the run's last scores are issued: the queries may go
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+              if (w.see[g].hi > 0) {
+                if (lead) umma_commit(ABAR(C::B_QEMPTY + g));
+                n_q ^= 1u << g;
+              }
+            next = attend_item<KV>(p, min(id + step, items - 1));  // while the products run
+            looked = true;
+          }
         }
-        if (!looked) next = attend_item<KV>(p, min(id + step, items - 1));
-        w = next;
-        id += step;
+        use += 2 * count;
       }
+      if (!looked) next = attend_item<KV>(p, min(id + step, items - 1));
+      w = next;
+      id += step;
+    }
+    if (lead) {
       umma_commit(ABAR(C::B_END));
       wait_drain(ABAR(C::B_END), 0);  // nothing of ours may run on after the CTA frees TMEM
     }
+    __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------------- queries; paged: rows nobody may see, codes
     bool ok = true;
@@ -612,24 +668,14 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[0][k] = o[1][k] = 0u;
         }
-        if (!real) continue;
+        if (!split_out) {
+          store_rows32(p.O + ch * 32, real ? int64_t(row) * D : -1, o, inv);
+        } else if (real) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (split_out) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              reinterpret_cast<float4*>(p.part + at * D + ch * 32 + h * 16)[k] =
-                  make_float4(__uint_as_float(o[h][4 * k]) * inv, __uint_as_float(o[h][4 * k + 1]) * inv,
-                              __uint_as_float(o[h][4 * k + 2]) * inv, __uint_as_float(o[h][4 * k + 3]) * inv);
-          } else {
-            uint32_t x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              x[k] = pack_bf16x2(__uint_as_float(o[h][2 * k]) * inv, __uint_as_float(o[h][2 * k + 1]) * inv);
-            uint4* dst = reinterpret_cast<uint4*>(p.O + row * D + ch * 32 + h * 16);
-            dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
-            dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
-          }
+          for (int k = 0; k < 8; ++k)
+            reinterpret_cast<float4*>(p.part + at * D + ch * 32)[k] = make_float4(
+                __uint_as_float(o[k >> 2][4 * (k & 3)]) * inv, __uint_as_float(o[k >> 2][4 * (k & 3) + 1]) * inv,
+                __uint_as_float(o[k >> 2][4 * (k & 3) + 2]) * inv, __uint_as_float(o[k >> 2][4 * (k & 3) + 3]) * inv);
         }
       }
       __syncwarp();
