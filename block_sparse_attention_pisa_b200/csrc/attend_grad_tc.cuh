@@ -627,19 +627,23 @@ attend_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 #undef ABAR
 }
 
-// Adds up the runs of the key tiles that were cut, in run order: one block per key tile and key head.
+// Adds up the runs of the key tiles that were cut, in run order: kJoinSlices blocks per key tile and
+// key head, each a slice of its dV and dK, a row's 4 columns per thread and step.
+constexpr int kJoinSlices = 16;
 template <int D>
 __global__ void __launch_bounds__(256) attend_dkv_join_kernel(const AttendGradParams p) {
-  const int kts = (p.N + 127) / 128, kt = blockIdx.x % kts, bh = blockIdx.x / kts;
+  const int kts = (p.N + 127) / 128, kt = blockIdx.x / kJoinSlices % kts, bh = blockIdx.x / kJoinSlices / kts;
   if (query_runs((p.Hq / p.Hkv) * QueryRange(p.win, kt, p.N).count, p.run) <= 1) return;
   const RunAt f = find_run(p, -1, kt);  // every warp finds the same
-  const float* src = p.part + (size_t(bh) * p.slots + f.slot) * (2 * 128 * D);
-  for (int e = threadIdx.x * 4; e < 2 * 128 * D; e += 1024) {
+  constexpr int ALL = 2 * 128 * D, SLICE = ALL / kJoinSlices;
+  const float* src = p.part + (size_t(bh) * p.slots + f.slot) * ALL;
+  for (int e = blockIdx.x % kJoinSlices * SLICE + threadIdx.x * 4, end = (blockIdx.x % kJoinSlices + 1) * SLICE; e < end; e += 1024) {
     const int g = e / (128 * D), j = kt * 128 + (e / D) % 128, c = e % D;
     if (j >= p.N) continue;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int r = 0; r < f.runs; ++r) {
-      const float4 x = *reinterpret_cast<const float4*>(src + size_t(r) * (2 * 128 * D) + e);
+      const float4 x = *reinterpret_cast<const float4*>(src + size_t(r) * ALL + e);
       a.x += x.x;
       a.y += x.y;
       a.z += x.z;

@@ -37,8 +37,6 @@
 // CTA) and attend_token_join_kernel adds them in order.
 #pragma once
 
-#include <cuda_fp16.h>
-
 #include <type_traits>
 
 #include "attend_tc.cuh"
@@ -184,9 +182,6 @@ __device__ __forceinline__ void join_warps(const AttendTokenParams& p, const Tok
   }
 }
 
-// the power of two with these bits in its fp32 exponent field
-__device__ __forceinline__ float exponent(int field) { return __uint_as_float(uint32_t(field) << 23); }
-
 // D = A(16x16 fp16, row) * B(16x8 fp16, col) + D, fp32 accumulate.
 __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -194,21 +189,6 @@ __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint3
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// The low (high) two e4m3 codes of a word -> two fp16, exact (codes of NaN too).
-__device__ __forceinline__ uint32_t codes_to_f16_lo(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t codes_to_f16_hi(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  __half2 r = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&r);
 }
 // 8 x 8 16-bit matrix, a row per four lanes, transposed across the warp
 __device__ __forceinline__ uint32_t transpose8(uint32_t w) {

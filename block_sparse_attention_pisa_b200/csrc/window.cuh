@@ -7,6 +7,7 @@
 // [0, min(sinks, hi)) and the window [max(0, p0 - left), hi) with hi = min(n, p1 + right + 1).
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -66,4 +67,22 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
+// the power of two with these bits in its fp32 exponent field
+__device__ __forceinline__ float exponent(int field) { return __uint_as_float(uint32_t(field) << 23); }
+
+// The low (high) two e4m3 codes of a word -> two fp16, exact (codes of NaN too).
+__device__ __forceinline__ uint32_t codes_to_f16_lo(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes_to_f16_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&r);
+}
 }  // namespace pisa
