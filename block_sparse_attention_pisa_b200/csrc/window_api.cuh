@@ -93,6 +93,22 @@ pisa_status_t launch_cache(Kernel k, const pisa::CacheParams& p, int d, int sms,
   return check_launch(what);
 }
 
+// make_map with a box of box2 slices: tiles of several heads' tokens
+pisa_status_t make_rows_map(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box1,
+                            uint32_t box2) {
+  auto fn = encode_fn();
+  if (!fn) return fail(PISA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[3] = {d0, d1, d2};
+  cuuint64_t strides[2] = {d0 * 2, d0 * d1 * 2};
+  cuuint32_t box[3] = {64, box1, box2};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PISA_ERR_CUDA, "cuTensorMapEncodeTiled (rows) failed (%d)", int(r));
+  return ok();
+}
+
 // codes of 8 bits [d2][d1][d0], box {d0, box1, 1}, rows contiguous in shared memory
 pisa_status_t make_code_map(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box1) {
   auto fn = encode_fn();
@@ -108,20 +124,22 @@ pisa_status_t make_code_map(CUtensorMap* m, const void* ptr, uint64_t d0, uint64
   return ok();
 }
 
-// Row tiles, and the runs that their key tiles are cut into so that few rows over a long cache
-// still fill the SMs. Time goes as waves of (tiles of a run + an item's own cost, about one tile;
-// two with the partial sums of a cut one): the cut with the least is taken, of at least two tiles
-// a run.
+// Pieces of two row tiles, and the runs that their tiles are cut into so that few rows over a long
+// cache still fill the SMs. Time goes as waves of (tiles of a run + a piece's own cost, about two
+// tiles; three with the partial sums of a cut one): the cut with the least is taken, of at least
+// two tiles a run.
 constexpr int kSms = 148;
 void plan_attend(pisa::AttendTcParams* p, int64_t keys) {
   p->rt = pisa::RowTiles::of(p->Hq / p->Hkv);
-  p->tiles = p->rt.parts * int((int64_t(p->N) + p->rt.tokens - 1) / p->rt.tokens);
-  const int64_t pieces = int64_t(p->B) * p->Hkv * p->tiles, tiles = (keys + 127) / 128;
+  p->G = p->Hq / p->Hkv;
+  p->part_pairs = int((int64_t(p->N) + 2 * p->rt.tokens - 1) / (2 * p->rt.tokens));
+  p->pairs = p->rt.parts * p->part_pairs;
+  const int64_t pieces = int64_t(p->B) * p->Hkv * p->pairs, tiles = (keys + 127) / 128;
   int64_t best = 1;
   double least = 1e300;
   for (int64_t s = 1; s <= kSms && (s == 1 || (s <= tiles / 2 && (s - 1) * pieces < 2 * kSms)); ++s) {
     const double waves = double((pieces * s + kSms - 1) / kSms);
-    const double cost = waves * (double((tiles + s - 1) / s) + (s > 1 ? 2.0 : 1.0));
+    const double cost = waves * (double((tiles + s - 1) / s) + (s > 1 ? 3.0 : 2.0));
     if (cost < least * 0.97) {
       least = cost;
       best = s;
@@ -138,7 +156,8 @@ template <int D, int KV>
 pisa_status_t launch_attend_tc(pisa::AttendTcParams p, const void* K, const void* V, int page, int num_pages,
                                void* workspace, cudaStream_t st) {
   using C = pisa::AttendTcCfg<D, KV>;
-  CUtensorMap mK, mV;
+  CUtensorMap mQ, mK, mV;
+  PISA_TRY(make_rows_map(&mQ, p.Q, D, uint64_t(p.N), uint64_t(p.B) * p.Hq, uint32_t(p.rt.tokens), uint32_t(p.rt.heads)));
   if constexpr (KV == pisa::kKvPlain) {
     PISA_TRY(make_map(&mK, K, D, uint64_t(p.N), uint64_t(p.B) * p.Hkv, 128));
     PISA_TRY(make_map(&mV, V, D, uint64_t(p.N), uint64_t(p.B) * p.Hkv, 128));
@@ -156,7 +175,7 @@ pisa_status_t launch_attend_tc(pisa::AttendTcParams p, const void* K, const void
   }
   auto k = pisa::attend_tc_kernel<D, KV>;
   PISA_TRY(set_smem(k, C::SMEM));
-  k<<<unsigned(p.items < kSms ? p.items : kSms), C::kThreads, C::SMEM, st>>>(mK, mV, p);
+  k<<<unsigned(p.items < kSms ? p.items : kSms), C::kThreads, C::SMEM, st>>>(mQ, mK, mV, p);
   PISA_TRY(check_launch("attend_tc_kernel"));
   if (p.splits > 1) {
     pisa::attend_join_kernel<D><<<unsigned((rows + 3) / 4), 128, 0, st>>>(p, KV != pisa::kKvPlain);
