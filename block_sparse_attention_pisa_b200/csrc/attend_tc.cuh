@@ -375,56 +375,53 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   // Every role walks the CTA's items; counters of ring stages and barrier phases run on.
   if (warp == 0) {
     // ------------------------------------------------------------- producer
-    // Lanes 0 and 1 issue the two 64-column panels of a tile (D = 64: lane 0 alone); of an item's
-    // i-th tile, K is stage use 2 i and V 2 i + 1 behind the items before.
-    if (lane < 2) {
-      bool ok = true;
-      int use = 0;
-      constexpr int NL = C::NL;  // the stages that the copies land in: the ring's, or those for codes
-      for (ItemWalk at(p); at.more(p) && ok; at.advance(p)) {
-        const AttendItem w = attend_item<KV>(p, at);
-        if (!w.real) continue;
-        for (int i = w.tiles.from; i < w.tiles.to && ok; ++i) {
-          const int j0 = w.tiles.key(i);
-          for (int kv = 0; kv < 2 && ok; ++kv, ++use) {
-            const int s = use % NL;
-            ok = wait_bounded(ABAR((C::CODES ? C::B_LEMPTY : C::B_EMPTY) + s), ((use / NL) & 1) ^ 1, abort_flag);
-            ok = __all_sync(0x3u, ok);
-            if (!ok) break;
-            const uint32_t dst = base_u + (C::CODES ? C::OFF_CODES + s * C::LAND : C::OFF_RING + s * C::TILE);
-            if constexpr (KV == kKvPlain) {
-              if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_FULL + s), C::TILE);
-              __syncwarp(0x3u);
-              if (lane * 64 < D)
-                tma_load_3d(dst + lane * 16384, kv ? &tmV : &tmK, ABAR(C::B_FULL + s), lane * 64, j0, w.bh);
-            } else {
-              // pages that no row of the CTA sees, or that the table does not hold, stay out
-              const int per = 128 >> p.pages.log_page, size = 1 << p.pages.log_page;
-              uint32_t held = 0;
-              for (int q = 0; q < per; ++q)
-                if (w.both.any(j0 + q * size, size) && page_of(p.pages, w.b, j0 + q * size) >= 0) held |= 1u << q;
-              if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_LAND + s), __popc(held) * size * D * (C::CODES ? 1 : 2));
-              __syncwarp(0x3u);
-              if constexpr (C::CODES) {  // whole rows of D codes, lanes by turns
-                for (int q = lane; q < per; q += 2)
-                  if ((held >> q) & 1u)
-                    tma_load_3d(dst + q * size * D, kv ? &tmV : &tmK, ABAR(C::B_LAND + s), 0, 0,
-                                page_of(p.pages, w.b, j0 + q * size) * p.Hkv + w.hk);
-              } else if (lane * 64 < D) {
-                for (int q = 0; q < per; ++q)
-                  if ((held >> q) & 1u)
-                    tma_load_3d(dst + lane * 16384 + q * size * 128, kv ? &tmV : &tmK, ABAR(C::B_LAND + s), lane * 64, 0,
-                                page_of(p.pages, w.b, j0 + q * size) * p.Hkv + w.hk);
-              }
-            }
+    // Of an item's i-th tile, K is stage use 2 i and V 2 i + 1 behind the items before. Plain keys: lanes
+    // 0 and 1 issue the two 64-column panels (D = 64: lane 0 alone). Pages: lane q looks page q of the
+    // tile up (a tile ahead), and a copy per page and panel is issued by a lane of its own.
+    bool ok = true;
+    int use = 0;
+    constexpr int NL = C::NL;  // the stages that the copies land in: the ring's, or those for codes
+    for (ItemWalk at(p); at.more(p) && ok; at.advance(p)) {
+      const AttendItem w = attend_item<KV>(p, at);
+      if (!w.real) continue;
+      const int per = 128 >> p.pages.log_page, size = 1 << p.pages.log_page;
+      // pages that no row of the item sees, or that the table does not hold, stay out
+      auto page_at = [&](int i) -> int {
+        if (KV == kKvPlain || i >= w.tiles.to || lane >= per) return -1;
+        const int j = w.tiles.key(i) + lane * size;
+        return w.both.any(j, size) ? page_of(p.pages, w.b, j) : -1;
+      };
+      int ahead = page_at(w.tiles.from);
+      for (int i = w.tiles.from; i < w.tiles.to && ok; ++i) {
+        const int j0 = w.tiles.key(i);
+        const int page = __shfl_sync(0xffffffffu, ahead, lane & (per - 1));
+        const int held = __popc(__ballot_sync(0xffffffffu, ahead >= 0));
+        ahead = page_at(i + 1);
+        for (int kv = 0; kv < 2 && ok; ++kv, ++use) {
+          const int s = use % NL;
+          ok = __all_sync(0xffffffffu, wait_bounded(ABAR((C::CODES ? C::B_LEMPTY : C::B_EMPTY) + s), ((use / NL) & 1) ^ 1, abort_flag));
+          if (!ok) break;
+          const uint32_t dst = base_u + (C::CODES ? C::OFF_CODES + s * C::LAND : C::OFF_RING + s * C::TILE);
+          if constexpr (KV == kKvPlain) {
+            if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_FULL + s), C::TILE);
+            __syncwarp();
+            if (lane * 64 < D)
+              tma_load_3d(dst + lane * 16384, kv ? &tmV : &tmK, ABAR(C::B_FULL + s), lane * 64, j0, w.bh);
+          } else {
+            if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_LAND + s), held * size * D * (C::CODES ? 1 : 2));
+            __syncwarp();
+            const int q = lane & (per - 1), panel = lane / per;  // whole rows of codes are one panel
+            if (page >= 0 && panel < (C::CODES ? 1 : D / 64))
+              tma_load_3d(dst + (C::CODES ? q * size * D : panel * 16384 + q * size * 128), kv ? &tmV : &tmK,
+                          ABAR(C::B_LAND + s), panel * 64, 0, page * p.Hkv + w.hk);
           }
         }
       }
-      // no copy may still be in flight when the CTA exits
-      constexpr int landed = KV == kKvPlain ? C::B_FULL : C::B_LAND;
-      if (lane == 0)
-        for (int u = use > NL ? use - NL : 0; u < use; ++u) wait_drain(ABAR(landed + u % NL), (u / NL) & 1);
     }
+    // no copy may still be in flight when the CTA exits
+    constexpr int landed = KV == kKvPlain ? C::B_FULL : C::B_LAND;
+    if (lane == 0)
+      for (int u = use > NL ? use - NL : 0; u < use; ++u) wait_drain(ABAR(landed + u % NL), (u / NL) & 1);
   } else if (warp == 1) {
     // ------------------------------------------------------------- products
     constexpr uint32_t idS = idesc_bf16(128, 128, false), idO = idesc_bf16(128, D, true);
@@ -547,30 +544,37 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       if constexpr (KV == kKvPagedE4m3) {
         // 16 codes per thread and step -> 32 bytes of the swizzled operand; rows that nobody may
-        // see become zero. The scales stay out: scores and weights take them exactly in fp32.
-        const int ct = threadIdx.x - 64;
-        constexpr int CH = D / 16;  // 16-code chunks of a row
+        // see become zero. The scales stay out: scores and weights take them exactly in fp32. A
+        // thread keeps its chunk of the rows and its row's place in the swizzle: steps are offsets.
+        constexpr int CH = D / 16, STEP = 64 / CH;  // 16-code chunks of a row, rows of a step
+        const int ct = threadIdx.x - 64, c = ct % CH, r0 = ct / CH, c0 = (2 * c) & 7;
+        const uint32_t from = C::OFF_CODES + r0 * D + c * 16, to = C::OFF_RING + (c >> 2) * 16384 + r0 * 128;
+        const uint32_t at_lo = (c0 ^ (r0 & 7)) << 4, at_hi = ((c0 + 1) ^ (r0 & 7)) << 4;
         for (int u = use; u < use + 2 * count; ++u) {
           const int sl = u % C::NL, s = u % C::NS, j0 = w.tiles.key(w.tiles.from + ((u - use) >> 1));
           const uint32_t held = held_pages(p.pages, w.b, w.both, j0, lane);
+          const bool inner = (j0 + 128 <= w.both.sk || (j0 >= w.both.lo && j0 + 128 <= w.both.hi)) &&
+                             held == (1u << (128 >> p.pages.log_page)) - 1u;
           ok = wait_bounded(ABAR(C::B_EMPTY + s), ((u / C::NS) & 1) ^ 1, abort_flag) &&
                wait_bounded(ABAR(C::B_LAND + sl), (u / C::NL) & 1, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          const uint8_t* src = base + from + sl * C::LAND;
+          uint8_t* dst = base + to + s * C::TILE;
 #pragma unroll 4
-          for (int x = ct; x < 128 * CH; x += 64) {
-            const int r = x / CH, c = x % CH, j = j0 + r;
-            uint4 code = *reinterpret_cast<const uint4*>(base + C::OFF_CODES + sl * C::LAND + r * D + c * 16);
-            const bool in = ((held >> (r >> p.pages.log_page)) & 1u) && (j < w.both.sk || (j >= w.both.lo && j < w.both.hi));
-            if (!in) code = make_uint4(0, 0, 0, 0);
-            const uint4 lo = make_uint4(e4m3x2_to_bf16x2(code.x), e4m3x2_to_bf16x2(code.x >> 16),
-                                        e4m3x2_to_bf16x2(code.y), e4m3x2_to_bf16x2(code.y >> 16));
-            const uint4 hi = make_uint4(e4m3x2_to_bf16x2(code.z), e4m3x2_to_bf16x2(code.z >> 16),
-                                        e4m3x2_to_bf16x2(code.w), e4m3x2_to_bf16x2(code.w >> 16));
-            uint8_t* dst = base + C::OFF_RING + s * C::TILE + (c >> 2) * 16384 + r * 128;
-            const int c0 = (2 * c) & 7;
-            *reinterpret_cast<uint4*>(dst + ((c0 ^ (r & 7)) << 4)) = lo;
-            *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = hi;
+          for (int x = 0; x < 128 / STEP; ++x) {
+            uint4 code = *reinterpret_cast<const uint4*>(src + x * STEP * D);
+            if (!inner) {
+              const int r = r0 + x * STEP, j = j0 + r;
+              const bool in = ((held >> (r >> p.pages.log_page)) & 1u) && (j < w.both.sk || (j >= w.both.lo && j < w.both.hi));
+              if (!in) code = make_uint4(0, 0, 0, 0);
+            }
+            *reinterpret_cast<uint4*>(dst + x * STEP * 128 + at_lo) =
+                make_uint4(e4m3x2_to_bf16x2(code.x), e4m3x2_to_bf16x2(code.x >> 16), e4m3x2_to_bf16x2(code.y),
+                           e4m3x2_to_bf16x2(code.y >> 16));
+            *reinterpret_cast<uint4*>(dst + x * STEP * 128 + at_hi) =
+                make_uint4(e4m3x2_to_bf16x2(code.z), e4m3x2_to_bf16x2(code.z >> 16), e4m3x2_to_bf16x2(code.w),
+                           e4m3x2_to_bf16x2(code.w >> 16));
           }
           fence_proxy_async_smem();
           warp_arrive(ABAR(C::B_FULL + s));
