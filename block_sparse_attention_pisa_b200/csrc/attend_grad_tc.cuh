@@ -7,8 +7,8 @@
 // independently, by two threads or two groups of threads at once. Two kernels compute the
 // scores anew rather than add dQ up with atomics: their sums run in a fixed order.
 //
-// attend_dq_kernel: a CTA takes 128 rows of a key head (rows as in the forward kernel: the
-// group's heads packed, token-major) and walks the key tiles that they see. Tensor memory:
+// attend_dq_kernel: a CTA takes a row tile of a key head (as the forward kernel's) and walks the key
+// tiles that it sees. Tensor memory:
 // dQ (D columns), S in two buffers and dP in one (128 columns each); dS in bf16 overwrites
 // its S. Tile i + 1's S and (as soon as the row threads hold dP(i) in registers) dP are
 // issued before dS(i) is awaited, so the weights are computed under the products. It also
@@ -40,6 +40,7 @@ struct AttendGradParams {
   bf16 *dQ, *dK, *dV;
   float* part;  // runs of split key tiles: fp32 [slot][dV, dK][128][D]
   int B, Hq, Hkv, N;
+  RowTiles rt;
   Window win;
   float scale;
   int run;      // query tiles per run, at most
@@ -52,12 +53,16 @@ template <int D>
 struct AttendDqCfg {
   static constexpr int kThreads = 384;
   static constexpr int TILE = 128 * D * 2;
-  static constexpr int NS = D == 128 ? 5 : 10;
-  static constexpr int OFF_Q = 0, OFF_DO = TILE, OFF_RING = 2 * TILE;
-  static constexpr int OFF_X = OFF_RING + NS * TILE;  // float [2][128]: halves of delta
+  // K is held from its scores to its dQ product, V only for dP: rings of their own, so that V of the
+  // next tile does not queue behind K of the last
+  static constexpr int NK = D == 128 ? 3 : 5, NV = D == 128 ? 2 : 4;
+  static constexpr int OFF_Q = 0, OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + NK * TILE;
+  static constexpr int OFF_X = OFF_V + NV * TILE;  // float [2][128]: halves of delta
   static constexpr int OFF_BAR = OFF_X + 1024;
-  static constexpr int B_FULL = 0, B_EMPTY = B_FULL + NS, B_Q = B_EMPTY + NS;
-  static constexpr int B_SD = B_Q + 1;   // S and dP ready (commit)
+  static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + NK, B_VFULL = B_KEMPTY + NK, B_VEMPTY = B_VFULL + NV;
+  static constexpr int B_Q = B_VEMPTY + NV;  // Q, dO and O (in the last V stage) landed
+  static constexpr int B_X = B_Q + 1;        // delta computed: that stage is V's (8 warps)
+  static constexpr int B_SD = B_X + 1;   // S and dP ready (commit)
   static constexpr int B_R = B_SD + 1;   // dP read (8 warps)
   static constexpr int B_DS = B_R + 1;   // dS written (8 warps)
   static constexpr int B_O = B_DS + 1;   // all products done (commit)
@@ -70,8 +75,9 @@ struct AttendDqCfg {
 
 template <int D>
 __global__ void __launch_bounds__(384, 1)
-attend_dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                 const AttendGradParams p) {
+attend_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+                 const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const AttendGradParams p) {
   using C = AttendDqCfg<D>;
   using namespace tc;
   extern __shared__ __align__(16) uint8_t attend_dq_smem[];
@@ -83,23 +89,28 @@ attend_dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #define ABAR(i) (bar0 + 8u * uint32_t(i))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const int G = p.Hq / p.Hkv, rows = p.N * G;
-  const int row_tiles = (rows + 127) / 128;
-  const int bh = blockIdx.x / row_tiles;
-  const int row0 = (row_tiles - 1 - blockIdx.x % row_tiles) * 128;  // causal: the rows with the most keys first
-  const int b = bh / p.Hkv, hk = bh % p.Hkv;
+  const int G = p.Hq / p.Hkv, tokens = p.rt.tokens;
+  const int part_tiles = (p.N + tokens - 1) / tokens, row_tiles = part_tiles * p.rt.parts;
+  const int bh = blockIdx.x / row_tiles, tile = blockIdx.x - bh * row_tiles, part = tile / part_tiles;
+  const int t0 = (part_tiles - 1 - (tile - part * part_tiles)) * tokens;  // causal: the rows with the most keys first
+  const int head0 = bh * G + part * 128, heads = min(p.rt.heads, G - part * 128);
   Sight see;
-  see.set(p.win, row0 / G, min(row0 + 127, rows - 1) / G, p.N);
+  see.set(p.win, t0, min(t0 + tokens, p.N) - 1, p.N);
   TileList tiles;
   tiles.set(see, 0, 1);
   const int count = tiles.to;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::NS; ++s) {
-      mbar_init(ABAR(C::B_FULL + s), 1);
-      mbar_init(ABAR(C::B_EMPTY + s), 1);
+    for (int s = 0; s < C::NK; ++s) {
+      mbar_init(ABAR(C::B_KFULL + s), 1);
+      mbar_init(ABAR(C::B_KEMPTY + s), 1);
     }
-    mbar_init(ABAR(C::B_Q), 8);
+    for (int s = 0; s < C::NV; ++s) {
+      mbar_init(ABAR(C::B_VFULL + s), 1);
+      mbar_init(ABAR(C::B_VEMPTY + s), 1);
+    }
+    mbar_init(ABAR(C::B_Q), 1);
+    mbar_init(ABAR(C::B_X), 8);
     mbar_init(ABAR(C::B_SD), 1);
     mbar_init(ABAR(C::B_R), 8);
     mbar_init(ABAR(C::B_DS), 8);
@@ -117,29 +128,48 @@ attend_dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const uint32_t tmem = *reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
 
   if (warp == 0) {
+    // lanes 0 and 1: the two 64-column panels
     if (lane < 2) {
       bool ok = true;
-      int use = 0;
-      for (int i = 0; i < count && ok; ++i)
-        for (int kv = 0; kv < 2 && ok; ++kv, ++use) {
-          const int s = use % C::NS;
-          ok = wait_bounded(ABAR(C::B_EMPTY + s), ((use / C::NS) & 1) ^ 1, abort_flag);
-          ok = __all_sync(0x3u, ok);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_FULL + s), C::TILE);
-          __syncwarp(0x3u);
-          if (lane * 64 < D)
-            tma_load_3d(base_u + C::OFF_RING + s * C::TILE + lane * 16384, kv ? &tmV : &tmK, ABAR(C::B_FULL + s),
-                        lane * 64, tiles.key(i), bh);
+      const uint32_t bytes = uint32_t(tokens * p.rt.heads * D * 2);
+      if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_Q), 3 * bytes);
+      __syncwarp(0x3u);
+      if (lane * 64 < D) {
+        tma_load_3d(base_u + C::OFF_Q + lane * 16384, &tmQ, ABAR(C::B_Q), lane * 64, t0, head0);
+        tma_load_3d(base_u + C::OFF_DO + lane * 16384, &tmG, ABAR(C::B_Q), lane * 64, t0, head0);
+        tma_load_3d(base_u + C::OFF_V + (C::NV - 1) * C::TILE + lane * 16384, &tmO, ABAR(C::B_Q), lane * 64, t0, head0);
+      }
+      int i = 0, v_used = 0;
+      for (; i < count && ok; ++i) {
+        const int sk = i % C::NK, sv = i % C::NV;
+        ok = __all_sync(0x3u, wait_bounded(ABAR(C::B_KEMPTY + sk), ((i / C::NK) & 1) ^ 1, abort_flag));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_KFULL + sk), C::TILE);
+        __syncwarp(0x3u);
+        if (lane * 64 < D)
+          tma_load_3d(base_u + C::OFF_K + sk * C::TILE + lane * 16384, &tmK, ABAR(C::B_KFULL + sk), lane * 64, tiles.key(i), bh);
+        if (i == C::NV - 1) ok = wait_bounded(ABAR(C::B_X), 0, abort_flag);  // O has been read
+        ok = __all_sync(0x3u, ok && wait_bounded(ABAR(C::B_VEMPTY + sv), ((i / C::NV) & 1) ^ 1, abort_flag));
+        if (!ok) {
+          ++i;  // this tile's K is in flight
+          break;
         }
-      if (lane == 0)
-        for (int u = use > C::NS ? use - C::NS : 0; u < use; ++u) wait_drain(ABAR(C::B_FULL + u % C::NS), (u / C::NS) & 1);
+        if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_VFULL + sv), C::TILE);
+        __syncwarp(0x3u);
+        if (lane * 64 < D)
+          tma_load_3d(base_u + C::OFF_V + sv * C::TILE + lane * 16384, &tmV, ABAR(C::B_VFULL + sv), lane * 64, tiles.key(i), bh);
+        v_used = i + 1;
+      }
+      // no copy may still be in flight when the CTA exits
+      if (lane == 0) {
+        wait_drain(ABAR(C::B_Q), 0);
+        for (int u = i > C::NK ? i - C::NK : 0; u < i; ++u) wait_drain(ABAR(C::B_KFULL + u % C::NK), (u / C::NK) & 1);
+        for (int u = v_used > C::NV ? v_used - C::NV : 0; u < v_used; ++u) wait_drain(ABAR(C::B_VFULL + u % C::NV), (u / C::NV) & 1);
+      }
     }
   } else if (warp == 1) {
     constexpr uint32_t idS = idesc_bf16(128, 128, false), idQ = idesc_bf16(128, D, true);
     const bool lead = elect();
-    auto stage = [&](int use) { return base_u + C::OFF_RING + (use % C::NS) * C::TILE; };
-    auto full = [&](int use) { return wait_warp(ABAR(C::B_FULL + use % C::NS), (use / C::NS) & 1, abort_flag); };
     auto rows_by = [&](uint32_t a, uint32_t t, uint32_t col) {  // A [128 rows][D] times the tile, transposed
       const uint64_t da = operand(a, 16), dt = operand(t, 16);
 #pragma unroll
@@ -150,30 +180,31 @@ attend_dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     };
     bool ok = wait_warp(ABAR(C::B_Q), 0, abort_flag);
     for (int i = -1; i < count && ok; ++i) {
-      if (i + 1 < count) {
-        if (!(ok = full(2 * i + 2))) break;
+      const int n = i + 1;
+      if (n < count) {
+        if (!(ok = wait_warp(ABAR(C::B_KFULL + n % C::NK), (n / C::NK) & 1, abort_flag))) break;
         tc_fence_after();
-        if (lead) rows_by(base_u + C::OFF_Q, stage(2 * i + 2), C::S_COL + ((i + 1) & 1) * 128);
+        if (lead) rows_by(base_u + C::OFF_Q, base_u + C::OFF_K + (n % C::NK) * C::TILE, C::S_COL + (n & 1) * 128);
         if (i >= 0 && !(ok = wait_warp(ABAR(C::B_R), i & 1, abort_flag))) break;
-        if (!(ok = full(2 * i + 3))) break;
+        if (!(ok = wait_warp(ABAR(C::B_VFULL + n % C::NV), (n / C::NV) & 1, abort_flag))) break;
         tc_fence_after();
         if (lead) {
-          rows_by(base_u + C::OFF_DO, stage(2 * i + 3), C::DP_COL);
+          rows_by(base_u + C::OFF_DO, base_u + C::OFF_V + (n % C::NV) * C::TILE, C::DP_COL);
           umma_commit(ABAR(C::B_SD));
-          umma_commit(ABAR(C::B_EMPTY + (2 * i + 3) % C::NS));
+          umma_commit(ABAR(C::B_VEMPTY + n % C::NV));
         }
       }
       if (i < 0) continue;
       if (!(ok = wait_warp(ABAR(C::B_DS), i & 1, abort_flag))) break;
       tc_fence_after();
       if (lead) {
-        const uint64_t k = operand(stage(2 * i), 16384);
+        const uint64_t k = operand(base_u + C::OFF_K + (i % C::NK) * C::TILE, 16384);
         const uint32_t ds = tmem + C::S_COL + (i & 1) * 128;
         // keys [16c, 16c + 16): the thread of half c / 4 packed them at the start of its columns
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           umma_ts(tmem + C::DQ_COL, ds + (c >> 2) * 64 + (c & 3) * 8, k + c * (2048 >> 4), idQ, (i | c) ? 1u : 0u);
-        umma_commit(ABAR(C::B_EMPTY + (2 * i) % C::NS));
+        umma_commit(ABAR(C::B_KEMPTY + i % C::NK));
       }
     }
     if (lead) {
@@ -184,42 +215,36 @@ attend_dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   } else if (warp >= 4) {
     // two threads per row: half hf has keys [64 hf, 64 hf + 64) of a tile, and D/2 dimensions
     const int hf = (warp - 4) >> 2, rt = threadIdx.x & 127;
-    const int r = row0 + rt;
-    const bool real = r < rows;
-    const int t = real ? r / G : 0, head = hk * G + (real ? r % G : 0);
-    const size_t row = (size_t(b) * p.Hq + head) * p.N + t;
+    const int my_head = rt / tokens, my_token = rt - my_head * tokens;
+    const bool real = my_head < heads && t0 + my_token < p.N;
+    const int t = t0 + (real ? my_token : 0);
+    const size_t row = size_t(head0 + (real ? my_head : 0)) * p.N + t;
     const uint32_t lrow = uint32_t((warp & 3) * 32) << 16;
+    bool ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_Q), 0, abort_flag));
     float delta = 0.f;
-    {
-      const uint4* q = reinterpret_cast<const uint4*>(p.Q + row * D + hf * (D / 2));
-      const uint4* g = reinterpret_cast<const uint4*>(p.dO + row * D + hf * (D / 2));
-      const uint4* o = reinterpret_cast<const uint4*>(p.O + row * D + hf * (D / 2));
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        const uint4 x = real ? __ldg(q + c) : zero, y = real ? __ldg(g + c) : zero, w = real ? __ldg(o + c) : zero;
-        const int ch = hf * (D / 16) + c;
-        const uint32_t off = (ch >> 3) * 16384 + rt * 128 + (((ch & 7) ^ (rt & 7)) << 4);
-        *reinterpret_cast<uint4*>(base + C::OFF_Q + off) = x;
-        *reinterpret_cast<uint4*>(base + C::OFF_DO + off) = y;
-        const uint32_t a[4] = {y.x, y.y, y.z, y.w}, e[4] = {w.x, w.y, w.z, w.w};
+    for (int c = 0; c < D / 16; ++c) {
+      const int ch = hf * (D / 16) + c;
+      const uint32_t off = (ch >> 3) * 16384 + rt * 128 + (((ch & 7) ^ (rt & 7)) << 4);
+      const uint4 y = *reinterpret_cast<const uint4*>(base + C::OFF_DO + off);
+      const uint4 w = *reinterpret_cast<const uint4*>(base + C::OFF_V + (C::NV - 1) * C::TILE + off);
+      const uint32_t a[4] = {y.x, y.y, y.z, y.w}, e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          delta = fmaf(bf16_lo(a[k]), bf16_lo(e[k]), delta);
-          delta = fmaf(bf16_hi(a[k]), bf16_hi(e[k]), delta);
-        }
+      for (int k = 0; k < 4; ++k) {
+        delta = fmaf(bf16_lo(a[k]), bf16_lo(e[k]), delta);
+        delta = fmaf(bf16_hi(a[k]), bf16_hi(e[k]), delta);
       }
     }
-    fence_proxy_async_smem();
-    warp_arrive(ABAR(C::B_Q));
+    fence_proxy_async_smem();  // reads of O before V's copies into its stage
+    warp_arrive(ABAR(C::B_X));
     float* xd = reinterpret_cast<float*>(base + C::OFF_X);
     xd[hf * 128 + rt] = delta;
-    bool ok = pair_sync_and(1 + (warp & 3), true);
+    ok = pair_sync_and(1 + (warp & 3), ok);
     delta = xd[rt] + xd[128 + rt];  // the same order on both sides
     if (real && hf == 0) p.delta[row] = delta;
     const float lse2 = real ? p.lse[row] * 1.4426950408889634f : 0.f, sl2 = p.scale * 1.4426950408889634f;
     const int z = min(p.N - 1, t + p.win.right), a = max(0, t - p.win.left);
-    for (int i = 0; i < count; ++i) {
+    for (int i = 0; i < count && ok; ++i) {
       const int j0 = tiles.key(i) + hf * 64;
       const bool whole = j0 + 63 <= see.p0 + p.win.right && j0 + 64 <= p.N &&
                          (j0 >= see.p1 - p.win.left || j0 + 64 <= p.win.sinks);
@@ -241,9 +266,11 @@ attend_dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       tc_fence_before();
       warp_arrive(ABAR(C::B_R));
 #pragma unroll
-      for (int k = 0; k < 64; ++k) {
-        const float w = ex2(fmaf(__uint_as_float(sc[k]), sl2, -lse2));
-        sc[k] = __float_as_uint(w * (__uint_as_float(dp[k]) - delta));
+      for (int k = 0; k < 64; k += 2) {
+        float e0 = __uint_as_float(sc[k]), e1 = __uint_as_float(sc[k + 1]);
+        fma2(e0, e1, sl2, -lse2);
+        sc[k] = __float_as_uint(ex2(e0) * (__uint_as_float(dp[k]) - delta));
+        sc[k + 1] = __float_as_uint(ex2(e1) * (__uint_as_float(dp[k + 1]) - delta));
       }
       if (!whole) {
 #pragma unroll
@@ -270,21 +297,15 @@ attend_dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     ok = __all_sync(0xffffffffu, ok && wait_bounded(ABAR(C::B_O), 0, abort_flag));
     tc_fence_after();
 #pragma unroll 1
-    for (int ch = 0; ch < D / 32; ++ch) {
+    for (int ch = 0; ch < D / 64; ++ch) {
       __syncwarp();
-      uint32_t x[16];
-      const int c0 = hf * (D / 2) + ch * 16;
-      tmem_ld16(tmem + lrow + C::DQ_COL + c0, x);
-      tmem_wait_ld(x);
-      if (real && ok) {
-        uint32_t w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          w[k] = pack_bf16x2(__uint_as_float(x[2 * k]) * p.scale, __uint_as_float(x[2 * k + 1]) * p.scale);
-        uint4* dst = reinterpret_cast<uint4*>(p.dQ + row * D + c0);
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      }
+      uint32_t x[2][16];
+      const int c0 = hf * (D / 2) + ch * 32;
+      tmem_ld16(tmem + lrow + C::DQ_COL + c0, x[0]);
+      tmem_ld16(tmem + lrow + C::DQ_COL + c0 + 16, x[1]);
+      tmem_wait_ld(x[0]);
+      tmem_wait_ld(x[1]);
+      store_rows32(p.dQ + c0, real && ok ? int64_t(row) * D : -1, x, p.scale);
     }
     tc_fence_before();
   }
@@ -592,30 +613,18 @@ attend_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const float f = g ? p.scale : 1.f;
     const uint32_t col = tmem + lrow + (g ? C::DK_COL : C::DV_COL);
     const size_t key = size_t(bh) * p.N + j;
-    float* part = p.part + (size_t(bh) * p.slots + misc[5] + run) * (2 * 128 * D) + (g * 128 + (threadIdx.x & 127)) * D;
-    bf16* out = (g ? p.dK : p.dV) + key * D;
+    float* part = p.part + (size_t(bh) * p.slots + misc[5] + run) * (2 * 128 * D) + g * 128 * D;
+    bf16* out = g ? p.dK : p.dV;
 #pragma unroll 1
-    for (int ch = 0; ch < D / 16; ++ch) {
+    for (int ch = 0; ch < D / 32; ++ch) {
       __syncwarp();
-      uint32_t x[16];
-      tmem_ld16(col + ch * 16, x);
-      tmem_wait_ld(x);
-      if (!ok) continue;
-      if (runs > 1) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          reinterpret_cast<float4*>(part + ch * 16)[k] =
-              make_float4(__uint_as_float(x[4 * k]) * f, __uint_as_float(x[4 * k + 1]) * f,
-                          __uint_as_float(x[4 * k + 2]) * f, __uint_as_float(x[4 * k + 3]) * f);
-      } else if (j < p.N) {
-        uint32_t w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          w[k] = pack_bf16x2(__uint_as_float(x[2 * k]) * f, __uint_as_float(x[2 * k + 1]) * f);
-        uint4* dst = reinterpret_cast<uint4*>(out + ch * 16);
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      }
+      uint32_t x[2][16];
+      tmem_ld16(col + ch * 32, x[0]);
+      tmem_ld16(col + ch * 32 + 16, x[1]);
+      tmem_wait_ld(x[0]);
+      tmem_wait_ld(x[1]);
+      if (runs > 1) store_part32(part + ch * 32, ok ? int64_t(threadIdx.x & 127) * D : -1, x, f);
+      else store_rows32(out + ch * 32, ok && j < p.N ? int64_t(key) * D : -1, x, f);
     }
     tc_fence_before();
   }

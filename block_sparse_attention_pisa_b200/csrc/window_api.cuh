@@ -265,20 +265,24 @@ GradPlan plan_grad(const pisa_window_shape_t& s, const pisa::Window& w) {
 
 template <int D>
 pisa_status_t launch_grad(pisa::AttendGradParams p, const GradPlan& g, const void* K, const void* V, cudaStream_t st) {
-  const uint64_t heads = uint64_t(p.B) * p.Hkv, N = uint64_t(p.N);
-  CUtensorMap mK, mV, mQ, mG;
+  const uint64_t heads = uint64_t(p.B) * p.Hkv, q_heads = uint64_t(p.B) * p.Hq, N = uint64_t(p.N);
+  p.rt = pisa::RowTiles::of(p.Hq / p.Hkv);
+  CUtensorMap mK, mV, mQ, mG, rQ, rG, rO;
+  PISA_TRY(make_rows_map(&rQ, p.Q, D, N, q_heads, uint32_t(p.rt.tokens), uint32_t(p.rt.heads)));
+  PISA_TRY(make_rows_map(&rG, p.dO, D, N, q_heads, uint32_t(p.rt.tokens), uint32_t(p.rt.heads)));
+  PISA_TRY(make_rows_map(&rO, p.O, D, N, q_heads, uint32_t(p.rt.tokens), uint32_t(p.rt.heads)));
   PISA_TRY(make_map(&mK, K, D, N, heads, 128));
   PISA_TRY(make_map(&mV, V, D, N, heads, 128));
-  PISA_TRY(make_map(&mQ, p.Q, D, N, uint64_t(p.B) * p.Hq, 64));
-  PISA_TRY(make_map(&mG, p.dO, D, N, uint64_t(p.B) * p.Hq, 64));
+  PISA_TRY(make_map(&mQ, p.Q, D, N, q_heads, 64));
+  PISA_TRY(make_map(&mG, p.dO, D, N, q_heads, 64));
   auto kq = pisa::attend_dq_kernel<D>;
   auto kk = pisa::attend_dkv_kernel<D>;
   using Cq = pisa::AttendDqCfg<D>;
   using Ck = pisa::AttendDkvCfg<D>;
   PISA_TRY(set_smem(kq, Cq::SMEM));
   PISA_TRY(set_smem(kk, Ck::SMEM));
-  const unsigned row_tiles = unsigned((int64_t(p.Hq / p.Hkv) * p.N + 127) / 128);
-  kq<<<row_tiles * unsigned(heads), Cq::kThreads, Cq::SMEM, st>>>(mK, mV, p);
+  const unsigned row_tiles = unsigned(p.rt.parts) * unsigned((p.N + p.rt.tokens - 1) / p.rt.tokens);
+  kq<<<row_tiles * unsigned(heads), Cq::kThreads, Cq::SMEM, st>>>(rQ, rG, rO, mK, mV, p);
   PISA_TRY(check_launch("attend_dq_kernel"));
   kk<<<unsigned(g.runs) * unsigned(heads), Ck::kThreads, Ck::SMEM, st>>>(mK, mV, mQ, mG, p);
   PISA_TRY(check_launch("attend_dkv_kernel"));
