@@ -17,8 +17,7 @@ namespace pisa {
 constexpr int kMaxTokens = 1 << 30;  // positions, window reaches and sinks stay below: sums fit 32 bits
 
 struct Window {
-  int left, right, sinks;  // reaches in [0, kMaxTokens]: kMaxTokens stands for no limit
-  __device__ __forceinline__ bool sees(int p, int j) const { return j <= p + right && (j >= p - left || j < sinks); }
+  int left, right, sinks;  // below kMaxTokens; kMaxTokens - 1 stands for no limit
 };
 
 enum { kKvPlain = 0, kKvPaged = 1, kKvPagedE4m3 = 2 };

@@ -238,9 +238,10 @@ pisa_status_t launch_token(const pisa::AttendTcParams& a, int ctas, void* worksp
   return check_launch("attend_token_join_kernel");
 }
 
-// How the key tiles of the gradient are cut into runs of query tiles: about two CTAs per SM if
-// all were equal, so that a tile which every row sees (the first tokens) is cut and the
-// window's are not.
+// How the key tiles of the gradient are cut into runs of query tiles: as if two CTAs per SM shared
+// all of them evenly, so that a tile which every row sees (the first tokens, or a causal sequence's
+// first keys) is cut and a window's are not. (Runs of the window's own length, with more partial sums,
+// measured 2% slower: 1306 against 1277 us for the step on 16384 tokens.)
 struct GradPlan {
   int run, runs, slots;
   size_t delta_bytes, bytes;

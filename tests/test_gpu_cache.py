@@ -404,3 +404,60 @@ def test_scales_of_every_size(N):
     O, lse = P.paged_attention(Q, cache, table, ints(lens))
     P.device_error()
     check_attention(O, lse, Q, cache, table, lens, [N] * 2, -1, 0, 0, d ** -0.5)
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^31 elements whose sequences lie in its last pages."""
+    Hkv, page, d = 8, 128, 128
+    num = 2 ** 31 // (Hkv * page * d) + 12
+    cache = P.PagedCache(*(torch.empty(num, Hkv, page, d, dtype=BF16, device="cuda") for _ in "KV"))
+    lens = [300, 130]
+    table = ints([[num - 1, num - 3, num - 2], [num - 7, num - 4, -1]])
+    K, V = randn(2, Hkv, 300, d, seed=41), randn(2, Hkv, 300, d, seed=42)
+    P.cache_write(K, V, cache, table, ints(lens), ints(lens))
+    back = P.cache_read(cache, table, ints(lens), 300)
+    for b, n in enumerate(lens):
+        assert torch.equal(back[0][b, :, :n], K[b, :, :n]) and torch.equal(back[1][b, :, :n], V[b, :, :n])
+    for N in (1, 24):
+        Q = randn(2, 16, N, d, seed=43)
+        O, lse = P.paged_attention(Q, cache, table, ints(lens))
+        P.device_error()
+        for b, n in enumerate(lens):
+            see = W.visible(n - N + np.arange(N), n, -1, 0, 0)
+            for h in (0, 15):
+                wo, wl, to, tl = T.forward(f64(Q)[b, h], f64(K)[b, h // 2, :n], f64(V)[b, h // 2, :n], see, d ** -0.5)
+                T.check(f64(O)[b, h], wo, to, "O")
+                T.check(f64(lse)[b, h], wl, tl, "lse")
+
+
+@pytest.mark.parametrize("N", [1, 20])
+def test_many_sequences(N):
+    """More sequences than a block has threads, of all lengths, some empty, some without new tokens."""
+    rng = np.random.default_rng(51)
+    lens = [int(x) for x in rng.integers(0, 70, 300)]
+    news = [min(int(x), n) for x, n in zip(rng.integers(0, N + 1, 300), lens)]
+    cache, table = filled(lens, 1, 16, 64, E4M3, seed=51)
+    Q = randn(300, 2, N, 64, seed=52)
+    O, lse = P.paged_attention(Q, cache, table, ints(lens), ints(news))
+    P.device_error()
+    check_attention(O, lse, Q, cache, table, lens, news, -1, 0, 0, 64 ** -0.5)
+    for b, m in enumerate(news):
+        assert (O[b, :, m:] == 0).all() and (lse[b, :, m:] == 0).all()
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams over one cache, each with its own workspace."""
+    lens = [3000, 40]
+    cache, table = filled(lens, 2, 64, 128, BF16, seed=53)
+    Q = [randn(2, 8, n, 128, seed=54) for n in (1, 1, 30)]
+    want = [P.paged_attention(q, cache, table, ints(lens)) for q in Q]
+    n = ints(lens)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in Q]
+    for _ in range(5):
+        got = []
+        for q, s in zip(Q, streams):
+            with torch.cuda.stream(s):
+                got.append(P.paged_attention(q, cache, table, n))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(want, got) for a, b in zip(x, y))

@@ -231,3 +231,36 @@ def test_empty_problem():
     O, lse = P.window_attention(Q, Q, Q)
     assert O.shape == Q.shape and lse.shape == (0, 2, 5)
     assert [g.shape for g in P.window_attention_backward(Q, Q, Q, Q, O, lse)] == [Q.shape] * 3
+
+
+def test_key_tiles_cut_into_many_runs():
+    """A causal sequence with many heads on one key head: its first key tiles are cut into runs."""
+    B, Hq, Hkv, N, d = 1, 6, 1, 1300, 64
+    Q, K, V, dO = make(B, Hq, Hkv, N, d, seed=21)
+    for mask in (dict(left=-1, right=0, sinks=0), dict(left=100, right=0, sinks=200)):
+        O, lse = P.window_attention(Q, K, V, **mask)
+        grads = P.window_attention_backward(dO, Q, K, V, O, lse, **mask)
+        P.device_error()
+        check_backward(grads, dO, Q, K, V, mask["left"], 0, mask["sinks"], d ** -0.5)
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams, each with its own workspace, give the bits of calls alone."""
+    args = [make(1, 4, 2, 900 + 100 * i, 128, seed=30 + i) for i in range(2)]
+    mask = dict(left=300, right=0, sinks=16)
+
+    def step(Q, K, V, dO):
+        O, lse = P.window_attention(Q, K, V, **mask)
+        return O, lse, *P.window_attention_backward(dO, Q, K, V, O, lse, **mask)
+
+    want = [step(*a) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    got = [None, None]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = step(*args[i])
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
