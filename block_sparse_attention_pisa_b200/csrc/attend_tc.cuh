@@ -84,7 +84,8 @@ struct AttendTcCfg {
   static constexpr int B_QEMPTY = B_Q + 2;          // [2] the item's last scores are done (commit)
   static constexpr int B_S = B_QEMPTY + 2;          // [2] S ready (commit)
   static constexpr int B_P = B_S + 2;               // [2] P written (4 warps)
-  static constexpr int B_O = B_P + 2;               // [2] the item's last product is done (commit)
+  static constexpr int B_H = B_P + 2;               // [2] the first half of P written (4 warps)
+  static constexpr int B_O = B_H + 2;               // [2] the item's last product is done (commit)
   static constexpr int B_END = B_O + 2;             // all products done (commit)
   static constexpr int NBARS = B_END + 1;
   static constexpr int OFF_BAR = OFF_SCALE + (CODES ? 8 * 2 * 128 * 4 : 0);
@@ -357,6 +358,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(ABAR(C::B_QEMPTY + g), 1);
       mbar_init(ABAR(C::B_S + g), 1);
       mbar_init(ABAR(C::B_P + g), 4);
+      mbar_init(ABAR(C::B_H + g), 4);
       mbar_init(ABAR(C::B_O + g), 1);
     }
     mbar_init(ABAR(C::B_END), 1);
@@ -454,16 +456,26 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           for (int g = 0; g < 2; ++g) {
             const bool saw = (before >> g) & 1u;
             // the group has awaited V of this tile and K of the next before it signals P
-            if (saw && !(ok = wait_warp(ABAR(C::B_P + g), (n_p >> g) & 1u, abort_flag) && full(use + 2*i+1))) break;
+            if (saw) {  // O += P V, by halves of the keys
+              if (!(ok = wait_warp(ABAR(C::B_H + g), (n_p >> g) & 1u, abort_flag))) break;
+              if (!(ok = full(use + 2 * i + 1))) break;
+              tc_fence_after();
+              if (lead) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  umma_ts(tmem + C::O_COL + g * D, tmem + C::S_COL + g * 128 + c * 8, v + c * (2048 >> 4), idO,
+                          (((has_o >> g) & 1u) | uint32_t(c)) ? 1u : 0u);
+              }
+              if (!(ok = wait_warp(ABAR(C::B_P + g), (n_p >> g) & 1u, abort_flag))) break;
+            }
             const bool sees = more && w.see[g].any(jn);
             if (sees && !(ok = full(use + 2 * i + 2))) break;
             tc_fence_after();
             if (lead) {
               if (saw) {  // O += P V
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  umma_ts(tmem + C::O_COL + g * D, tmem + C::S_COL + g * 128 + c * 8, v + c * (2048 >> 4), idO,
-                          (((has_o >> g) & 1u) | uint32_t(c)) ? 1u : 0u);
+                for (int c = 4; c < 8; ++c)
+                  umma_ts(tmem + C::O_COL + g * D, tmem + C::S_COL + g * 128 + c * 8, v + c * (2048 >> 4), idO, 1u);
                 if (i == last[g]) umma_commit(ABAR(C::B_O + g));
               }
               if (sees) {  // S = Q K^T of the next tile
@@ -705,13 +717,16 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               if (!((bits >> k) & 1u)) sc[32 * x + k] = __float_as_uint(-INFINITY);
           }
         }
-        float mxp[8];
+        float mxp[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mxp[k] = __uint_as_float(sc[k]);
+        for (int k = 0; k < 4; ++k) mxp[k] = __uint_as_float(sc[k]);
 #pragma unroll
-        for (int k = 8; k < 128; ++k) mxp[k & 7] = fmaxf(mxp[k & 7], __uint_as_float(sc[k]));
-        const float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
-                               fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7]))) * sl2;
+        for (int k = 4; k < 124; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mxp[e] = max3(mxp[e], __uint_as_float(sc[k + 2 * e]), __uint_as_float(sc[k + 2 * e + 1]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mxp[e] = fmaxf(mxp[e], __uint_as_float(sc[124 + e]));
+        const float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * sl2;
         const bool grow = mx > m + 8.f;
         const bool move = grow && m != -INFINITY;
         if (__any_sync(0xffffffffu, move)) {  // S(i) is behind every earlier product of the group
@@ -738,6 +753,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             }
           }
           tmem_st16(s_addr + ch * 16, pk);
+          if (ch == 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(ABAR(C::B_H + g));
+          }
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
