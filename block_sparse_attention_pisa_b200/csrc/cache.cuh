@@ -6,9 +6,10 @@
 // |x| and a NaN's lie above infinity's, so the maximum is taken over the bits: a row with an
 // infinity or a NaN gets the scale NaN, and the whole row reads back as NaN.
 //
-// Both kernels are bound by memory: each row of x is read once and its codes written once (or
-// the reverse). A thread takes 16 bytes of the cache's row (16 codes or 8 bf16) of K and of V,
-// kCacheRows rows in flight.
+// Both kernels read each row of x once and write its codes once (or the reverse). Reading back, and
+// bf16 both ways, a thread takes 16 bytes of the cache's row of K and of V, kCacheRows rows in
+// flight, and memory bounds it (130 us for 8 x 8 sequences of 9-16 K rows of 128: 4.9 TB/s, five
+// eighths of it writes). Quantising, a thread takes 32 values.
 #pragma once
 
 #include "window.cuh"
@@ -51,94 +52,121 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
          uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16;
 }
 
-// 16 bf16 of a row -> its scale and 16 codes.
-// The fp32 quotient x / scale by Markstein's correction (P. Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", 1990): with y the correctly
-// rounded reciprocal and q = x y, the remainder r = x - q scale is exact and q + r y is the
-// correctly rounded quotient, unless scale's mantissa is all ones or r leaves the range. Rows
-// of such scales (below 2^-90 the remainder could) divide. Three operations a value; with a
-// division for each the kernel was bound by issue (75 us for 2 x 24 x 4096 rows of 128).
+// The fp32 quotient a / b by Markstein's correction (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990): with y the correctly rounded
+// reciprocal of b and q = a y, the remainder r = a - q b is exact and q + r y is the correctly
+// rounded quotient, unless b's mantissa is all ones or r leaves the range.
+__device__ __forceinline__ float quotient(float a, float b, float y) {
+  const float q = a * y;
+  return fmaf(fmaf(-q, b, a), y, q);
+}
+
+// 32 bf16 of a row -> its scale and 32 codes. Three operations a value; rows whose scale Markstein's
+// correction does not cover (below 2^-90 its remainder could leave the range) divide. With a
+// division for each value the kernel was bound by issue (75 us for 2 x 24 x 4096 rows of 128), and
+// still was (50 us) with 16 values per thread, where the row's own work weighs twice as much.
 template <int LPR>
-__device__ __forceinline__ uint4 quantise16(const uint4& x0, const uint4& x1, float& scale) {
-  const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-  uint32_t top = 0;
+__device__ __forceinline__ void quantise32(const uint4 (&x)[4], float& scale, uint4 (&code)[2]) {
+  uint32_t w[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+  for (int i = 0; i < 4; ++i) {
+    w[4 * i] = x[i].x;
+    w[4 * i + 1] = x[i].y;
+    w[4 * i + 2] = x[i].z;
+    w[4 * i + 3] = x[i].w;
+  }
+  uint32_t top = 0;  // the maximum over the bits, a half of the word at a time
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+  top = max(top & 0xffffu, top >> 16);
 #pragma unroll
   for (int off = 1; off < LPR; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
   if (top >= 0x7f80u) top = 0x7fc0u;  // an infinity or a NaN: NaN for the row
-  scale = __fdiv_rn(__uint_as_float(top << 16), 448.f);
-  if (scale < 1.17549435e-38f) scale = 1.17549435e-38f;  // a NaN stays one
-  const bool divide = scale < 8.0779357e-28f || (__float_as_uint(scale) & 0x7fffffu) == 0x7fffffu;
-  uint32_t c[4];
+  const float amax = __uint_as_float(top << 16);
+  scale = quotient(amax, 448.f, 1.f / 448.f);
+  bool divide = scale < 8.0779357e-28f;  // 2^-90
+  if (divide) {
+    scale = __fdiv_rn(amax, 448.f);
+    if (scale < 1.17549435e-38f) scale = 1.17549435e-38f;
+  }
+  divide |= (__float_as_uint(scale) & 0x7fffffu) == 0x7fffffu;
+  uint32_t c[8];
   if (!divide) {
     const float y = __frcp_rn(scale);
-    auto quotient = [&](float x) {
-      const float q = x * y;
-      return fmaf(fmaf(-q, scale, x), y, q);
-    };
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c[i] = codes4(quotient(bf16_lo(w[2 * i])), quotient(bf16_hi(w[2 * i])), quotient(bf16_lo(w[2 * i + 1])),
-                    quotient(bf16_hi(w[2 * i + 1])));
+    for (int i = 0; i < 8; ++i)
+      c[i] = codes4(quotient(bf16_lo(w[2 * i]), scale, y), quotient(bf16_hi(w[2 * i]), scale, y),
+                    quotient(bf16_lo(w[2 * i + 1]), scale, y), quotient(bf16_hi(w[2 * i + 1]), scale, y));
   } else {
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {  // rolled: rare, and its code should stay small
-      const uint32_t a = i == 0 ? w[0] : i == 1 ? w[2] : i == 2 ? w[4] : w[6];
-      const uint32_t b = i == 0 ? w[1] : i == 1 ? w[3] : i == 2 ? w[5] : w[7];
-      const uint32_t x = codes4(__fdiv_rn(bf16_lo(a), scale), __fdiv_rn(bf16_hi(a), scale), __fdiv_rn(bf16_lo(b), scale),
+    for (int i = 0; i < 8; ++i) {  // rolled: rare, and its code should stay small
+      uint32_t a = 0, b = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k == i) {
+          a = w[2 * k];
+          b = w[2 * k + 1];
+        }
+      const uint32_t v = codes4(__fdiv_rn(bf16_lo(a), scale), __fdiv_rn(bf16_hi(a), scale), __fdiv_rn(bf16_lo(b), scale),
                                 __fdiv_rn(bf16_hi(b), scale));
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k == i) c[k] = x;
+      for (int k = 0; k < 8; ++k)
+        if (k == i) c[k] = v;
     }
   }
-  return make_uint4(c[0], c[1], c[2], c[3]);
+  code[0] = make_uint4(c[0], c[1], c[2], c[3]);
+  code[1] = make_uint4(c[4], c[5], c[6], c[7]);
 }
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheParams p) {
-  using C = CacheCfg<D, E4M3>;
-  constexpr int X = C::PER / 8;  // 16-byte loads of a row per thread
-  const int part = threadIdx.x % C::LPR, mine = threadIdx.x / C::LPR;
-  const int64_t step = int64_t(gridDim.x) * C::ROWS;
+  constexpr int PER = E4M3 ? 32 : 8, LPR = D / PER, ROWS = kCacheThreads / LPR;  // values, threads of a row; rows of a CTA
+  constexpr int FLY = E4M3 ? 1 : kCacheRows, X = PER / 8;  // rows in flight, 16-byte loads of each
+  const int part = threadIdx.x % LPR, mine = threadIdx.x / LPR;
+  const int64_t step = int64_t(gridDim.x) * ROWS;
   // every thread of a warp takes the same number of rounds (the shuffles need all lanes)
-  for (int64_t r0 = int64_t(blockIdx.x) * C::ROWS; r0 < p.rows; r0 += step * kCacheRows) {
-    uint4 k[kCacheRows][X], v[kCacheRows][X];
-    int64_t to[kCacheRows];
+  for (int64_t r0 = int64_t(blockIdx.x) * ROWS; r0 < p.rows; r0 += step * FLY) {
+    uint4 k[FLY][X], v[FLY][X];
+    int64_t to[FLY];
     // the values do not wait for the lengths and the table: a token that turns out not to be
     // real is read all the same (it lies inside K and V)
 #pragma unroll
-    for (int i = 0; i < kCacheRows; ++i) {
+    for (int i = 0; i < FLY; ++i) {
       const int64_t r = r0 + mine + i * step;
 #pragma unroll
       for (int x = 0; x < X; ++x) {
         k[i][x] = v[i][x] = make_uint4(0, 0, 0, 0);
         if (r < p.rows) {
-          k[i][x] = ldg_stream_v4(p.K + r * D + part * C::PER + x * 8);
-          v[i][x] = ldg_stream_v4(p.V + r * D + part * C::PER + x * 8);
+          k[i][x] = ldg_stream_v4(p.K + r * D + part * PER + x * 8);
+          v[i][x] = ldg_stream_v4(p.V + r * D + part * PER + x * 8);
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < kCacheRows; ++i) {
+    for (int i = 0; i < FLY; ++i) {
       const int64_t r = r0 + mine + i * step;
       to[i] = -1;
       if (r < p.rows) {
-        const uint32_t bh = uint32_t(r) / uint32_t(p.N), t = uint32_t(r) % uint32_t(p.N);
-        const int b = bh / p.Hkv, h = bh % p.Hkv;
+        const uint32_t bh = uint32_t(r) / uint32_t(p.N), t = uint32_t(r) - bh * uint32_t(p.N);
+        const int b = bh / p.Hkv, h = bh - b * p.Hkv;
         const int n = q_len_of(p.pages, b, p.N), pos = kv_len_of(p.pages, b) - n + int(t);
         if (int(t) < n && pos >= 0) to[i] = cache_row(p, b, h, pos);
       }
     }
 #pragma unroll
-    for (int i = 0; i < kCacheRows; ++i) {
+    for (int i = 0; i < FLY; ++i) {
       if constexpr (E4M3) {
         float ks, vs;
-        const uint4 kc = quantise16<C::LPR>(k[i][0], k[i][1], ks), vc = quantise16<C::LPR>(v[i][0], v[i][1], vs);
+        uint4 kc[2], vc[2];
+        quantise32<LPR>(k[i], ks, kc);
+        quantise32<LPR>(v[i], vs, vc);
         if (to[i] >= 0) {
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.cK) + to[i] * D + part * 16) = kc;
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.cV) + to[i] * D + part * 16) = vc;
+          uint4* dk = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.cK) + to[i] * D + part * 32);
+          uint4* dv = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.cV) + to[i] * D + part * 32);
+          dk[0] = kc[0];
+          dk[1] = kc[1];
+          dv[0] = vc[0];
+          dv[1] = vc[1];
           if (part == 0) {
             p.ks[to[i]] = ks;
             p.vs[to[i]] = vs;

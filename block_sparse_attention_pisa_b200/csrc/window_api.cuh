@@ -83,10 +83,11 @@ pisa_status_t check_cache(const pisa_cache_t& c, const pisa_sequences_t& s, int3
   return ok();
 }
 
-// the paged cache's kernels: 16 bytes of a cache row per thread, rows dealt out to the CTAs in turn
+// the paged cache's kernels: `values` of a row per thread, rows dealt out to the CTAs in turn
 template <typename Kernel>
-pisa_status_t launch_cache(Kernel k, const pisa::CacheParams& p, int d, int sms, cudaStream_t st, const char* what) {
-  const int64_t per = int64_t(pisa::kCacheThreads) * (p.ks || p.pages.ks ? 16 : 8) / d;
+pisa_status_t launch_cache(Kernel k, const pisa::CacheParams& p, int d, int values, int sms, cudaStream_t st,
+                           const char* what) {
+  const int64_t per = int64_t(pisa::kCacheThreads) * values / d;
   const int64_t ctas = (p.rows + per - 1) / per;
   const int64_t most = int64_t(sms) * 8;
   k<<<unsigned(ctas < most ? ctas : most), pisa::kCacheThreads, 0, st>>>(p);
@@ -402,7 +403,7 @@ pisa_status_t pisa_cache_write(const void* K, const void* V, pisa_cache_t cache,
   const bool q = cache.type == PISA_CACHE_E4M3;
   auto k = cache.d == 128 ? (q ? pisa::cache_write_kernel<128, true> : pisa::cache_write_kernel<128, false>)
                           : (q ? pisa::cache_write_kernel<64, true> : pisa::cache_write_kernel<64, false>);
-  return launch_cache(k, p, cache.d, sms, st, "cache_write_kernel");
+  return launch_cache(k, p, cache.d, q ? 32 : 8, sms, st, "cache_write_kernel");
 }
 
 pisa_status_t pisa_cache_read(pisa_cache_t cache, pisa_sequences_t seqs, void* K, void* V, void* stream) {
@@ -424,7 +425,7 @@ pisa_status_t pisa_cache_read(pisa_cache_t cache, pisa_sequences_t seqs, void* K
   const bool q = cache.type == PISA_CACHE_E4M3;
   auto k = cache.d == 128 ? (q ? pisa::cache_read_kernel<128, true> : pisa::cache_read_kernel<128, false>)
                           : (q ? pisa::cache_read_kernel<64, true> : pisa::cache_read_kernel<64, false>);
-  return launch_cache(k, p, cache.d, sms, st, "cache_read_kernel");
+  return launch_cache(k, p, cache.d, q ? 16 : 8, sms, st, "cache_read_kernel");
 }
 
 pisa_status_t pisa_paged_attention_workspace(pisa_cache_t cache, pisa_sequences_t seqs, int32_t Hq,
