@@ -8,8 +8,9 @@
 //
 // Both kernels read each row of x once and write its codes once (or the reverse). Reading back, and
 // bf16 both ways, a thread takes 16 bytes of the cache's row of K and of V, kCacheRows rows in
-// flight, and memory bounds it (130 us for 8 x 8 sequences of 9-16 K rows of 128: 4.9 TB/s, five
-// eighths of it writes). Quantising, a thread takes 32 values.
+// flight, and memory bounds it (126 us for 8 x 8 sequences of 9-16 K rows of 128: 5.1 TB/s, two
+// thirds of it writes; 131 us without streaming stores, 140 and 149 us with one and four rows in
+// flight). Quantising, a thread takes 32 values.
 #pragma once
 
 #include "window.cuh"
@@ -226,13 +227,13 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CachePa
       uint4* dk = reinterpret_cast<uint4*>(p.oK + (r0 + i * step) * D + part * C::PER);
       uint4* dv = reinterpret_cast<uint4*>(p.oV + (r0 + i * step) * D + part * C::PER);
       if constexpr (E4M3) {
-        dk[0] = restore8(k[i].x, k[i].y, ks[i]);
-        dk[1] = restore8(k[i].z, k[i].w, ks[i]);
-        dv[0] = restore8(v[i].x, v[i].y, vs[i]);
-        dv[1] = restore8(v[i].z, v[i].w, vs[i]);
+        __stcs(&dk[0], restore8(k[i].x, k[i].y, ks[i]));
+        __stcs(&dk[1], restore8(k[i].z, k[i].w, ks[i]));
+        __stcs(&dv[0], restore8(v[i].x, v[i].y, vs[i]));
+        __stcs(&dv[1], restore8(v[i].z, v[i].w, vs[i]));
       } else {
-        dk[0] = k[i];
-        dv[0] = v[i];
+        __stcs(&dk[0], k[i]);
+        __stcs(&dv[0], v[i]);
       }
     }
   }
