@@ -9,9 +9,9 @@
 // that walk the 128-key tiles that some row of theirs sees (the tiles of the first tokens, then the
 // window's); a group skips the ones that none of its rows sees. Warp roles:
 //   warp 0       producer: K and V tiles by TMA (a page at a time in a paged cache) into a ring,
-//                running ahead into the next item;
+//                running ahead into the next item; it publishes which pages of a tile are held;
 //   warp 1       issues every tcgen05.mma: per tile and group S = Q K^T (SS), then
-//                O += P V (TS, P from tensor memory);
+//                O += P V (TS, P from tensor memory), the latter in two halves;
 //   warp 3       loads the next item's queries once the last scores of this one are done;
 //   warp 2       paged caches: clears the rows of a V tile that no row may see (unwritten rows
 //                may hold anything, and 0 x NaN is NaN); 8 bits: warps 2-3 convert codes to bf16;
@@ -20,13 +20,28 @@
 // S) and O of either group (D columns each).
 //
 // The two groups alternate on the tensor core: while one group's exponentials run, the other's
-// P V and next Q K^T do. Products are issued by one lane and execute in order, so S of tile
-// i + 1 may overwrite P of tile i behind the P V that reads it, and a group that sees its S(i + 1)
-// (one commit) knows its O holds the products up to tile i: O is rescaled without a further
-// wait. The accumulator is rescaled only when the maximum grows by more than 2^8.
+// P V and next Q K^T do. A thread takes its whole row of S into registers, then hands P over in two
+// halves, so that the product over the first 64 keys runs under the exponentials of the others.
+// Products are issued by one lane and execute in order, so S of tile i + 1 may overwrite P of tile i
+// behind the P V that reads it, and a group that sees its S(i + 1) (one commit) knows its O holds
+// the products up to tile i: O is rescaled without a further wait. The accumulator is rescaled only
+// when the maximum grows by more than 2^8.
 //
-// Bound: at D = 128 a tile of 128 x 128 takes 2 x 512 cycles of tensor time and as long on the
-// exponential unit (16 per cycle and SM); at D = 64 the exponentials are twice the products.
+// A value that is no finite number and that only some rows of its tile see would reach the others
+// through a weight of zero. Looking at every such tile for it cost 5% (2 x 24 heads of 4096 x 128,
+// 512 keys to either side: 156 us against 148); the rows' output is looked at instead, and rows that
+// hold something that is no finite number are summed again (mend_rows).
+//
+// Bound: at D = 128 a tile of 128 x 128 takes 2 x 512 cycles of tensor time, and a pair of tiles
+// 2 x 512 x 2 = 2048, as long as its 2 x 16384 exponentials take at 16 per cycle. Measured, a pair
+// takes about 4000: the softmax of two rows per scheduler 2300 (exponential 8 cycles per warp and
+// instruction, the pack to bf16 as long again, two fma and add per value), and then, of either group,
+// the chain "second half of P V, next Q K^T, its commit" that the other group only partly covers.
+// 2 x 24 heads of 4096 x 128, 512 keys to either side: 148 us, 0.65 PFLOP/s; 2 x 1024 tokens of 24
+// heads over a paged cache of 16 K, window 8192: 265 us, 0.78 PFLOP/s; D = 64 has the same softmax for
+// half the products. What was tried and measured slower: one 128-row tile with two score buffers;
+// two threads per row; a maximum guessed from the tile before; separate columns for P; packed fp32
+// pairs for the scaling; setmaxnreg (the roles that give registers away spill).
 #pragma once
 
 #include "attention_tc.cuh"
@@ -52,7 +67,7 @@ struct AttendTcParams {
   float* lse;
   float* part;      // splits > 1: fp32 [splits][B * Hq * N][D], then base-2 lse [splits][B * Hq * N]
   float* part_lse;
-  Pages pages;      // paged only
+  Pages pages;      // paged; of plain keys K and V alone, [B * Hkv][N][D]
   int B, Hq, Hkv, N;
   RowTiles rt;
   int G;            // query heads per key head
@@ -78,7 +93,7 @@ struct AttendTcCfg {
   static constexpr int OFF_SCALE = OFF_CODES + NL * LAND;  // 8 bits: float [8 warps][K, V][128]
   static constexpr int B_FULL = 0;                  // [NS] stage holds its tile
   static constexpr int B_EMPTY = B_FULL + NS;       // [NS] products that read it are done (commit)
-  static constexpr int B_LAND = B_EMPTY + NS;       // [NL] paged: copies landed, rows not cleared yet
+  static constexpr int B_LAND = B_EMPTY + NS;       // [NL] paged: V landed, not cleared yet; codes not converted yet
   static constexpr int B_LEMPTY = B_LAND + NL;      // [NL] 8 bits: codes converted (2 warps)
   static constexpr int B_Q = B_LEMPTY + NL;         // [2] a group's queries are in shared memory
   static constexpr int B_QEMPTY = B_Q + 2;          // [2] the item's last scores are done (commit)
@@ -90,7 +105,10 @@ struct AttendTcCfg {
   static constexpr int NBARS = B_END + 1;
   static constexpr int OFF_BAR = OFF_SCALE + (CODES ? 8 * 2 * 128 * 4 : 0);
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBARS;
-  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  // Paged: bit i = page i of the tile is seen and held, for tile t at t % kHeld. Producer, converters
+  // and softmax are at most 7 tiles apart.
+  static constexpr int OFF_HELD = OFF_MISC + 16, kHeld = 16;
+  static constexpr int SMEM = OFF_HELD + 4 * kHeld + 1024;
   static constexpr int S_COL = 0, O_COL = 256;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -108,6 +126,10 @@ struct Sight {
   __device__ __forceinline__ void none() { p0 = p1 = lo = hi = sk = 0; }
   // some row may see a key of [j0, j0 + 128)
   __device__ __forceinline__ bool any(int j0) const { return j0 < sk || (j0 < hi && j0 + 128 > lo); }
+  // every row sees every key of [j0, j0 + 128)
+  __device__ __forceinline__ bool all(const Window& w, int j0, int n) const {
+    return j0 + 127 <= p0 + w.right && j0 + 128 <= n && (j0 >= p1 - w.left || j0 + 128 <= w.sinks);
+  }
   // some row may see a key of [j0, j0 + w)
   __device__ __forceinline__ bool any(int j0, int w) const { return j0 < sk || (j0 < hi && j0 + w > lo); }
 };
@@ -134,15 +156,26 @@ __device__ __forceinline__ uint32_t ones_below(int k) {  // bits [0, k) of a wor
   return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u);
 }
 
-// pages of the tile at j0 that `a` may see and the table holds: bit i = page i of the tile
-__device__ __forceinline__ uint32_t held_pages(const Pages& g, int b, const Sight& a, int j0, int lane) {
-  const int per = 128 >> g.log_page;
-  bool ok = false;
-  if (lane < per) {
-    const int j = j0 + (lane << g.log_page);
-    ok = a.any(j, 1 << g.log_page) && page_of(g, b, j) >= 0;
-  }
-  return __ballot_sync(0xffffffffu, ok);
+// Paged: parity on B_LAND of the stage that use `u` (odd: V) takes; K goes straight to B_FULL.
+template <int NS>
+__device__ __forceinline__ uint32_t landed_parity(int u) {
+  return uint32_t(NS % 2 ? u / (2 * NS) : u / NS) & 1u;
+}
+
+// bf16 values: any that is no finite number (an infinity or a NaN)
+__device__ __forceinline__ bool any_not_finite(uint4 v) {
+  constexpr uint32_t M = 0x7fff7fffu;
+  const uint32_t top = __vmaxu2(__vmaxu2(v.x & M, v.y & M), __vmaxu2(v.z & M, v.w & M));
+  return (top & 0x7f80u) == 0x7f80u || (top & 0x7f800000u) == 0x7f800000u;
+}
+// the low (high) half of a word as fp32 if it is no finite number, 0 if it is
+__device__ __forceinline__ float not_finite_lo(uint32_t w) { return (w & 0x7f80u) == 0x7f80u ? __uint_as_float(w << 16) : 0.f; }
+__device__ __forceinline__ float not_finite_hi(uint32_t w) {
+  return (w & 0x7f800000u) == 0x7f800000u ? __uint_as_float(w & 0xffff0000u) : 0.f;
+}
+// two values with those that are no finite numbers as 0
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
+  return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
 }
 
 // A 128-byte swizzled operand at `saddr` as its descriptor; a product's step adds its offset in
@@ -199,20 +232,13 @@ __device__ __forceinline__ void store_rows32(bf16* dst, int64_t at, const uint32
   }
 }
 
-// fp32 pairs: x = x * a + b, sum += x
+// fp32 pair: x = x * a + b
 __device__ __forceinline__ void fma2(float& x0, float& x1, float a, float b) {
   asm("{\n\t.reg .b64 x, y, z;\n\t"
       "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
       "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "+f"(x0), "+f"(x1)
       : "f"(a), "f"(b));
-}
-__device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
-  asm("{\n\t.reg .b64 x, y;\n\t"
-      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
-      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "+f"(s0), "+f"(s1)
-      : "f"(x0), "f"(x1));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -235,19 +261,6 @@ __device__ __forceinline__ void store_part32(float* dst, int64_t at, const uint3
       if (to >= 0) *reinterpret_cast<uint4*>(dst + to + h * 16 + q * 4) = make_uint4(c[j][0], c[j][1], c[j][2], c[j][3]);
     }
   }
-}
-
-// fp16 operands: idesc_bf16 with the 16-bit format of both operands fp16
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) { return tc::idesc_bf16(M, N, false) & ~((1u << 7) | (1u << 10)); }
-
-// The power of two that brings the largest value of a bf16 row to [2^14, 2^15); NaN for a row with
-// an infinity or a NaN.
-template <int W>
-__device__ __forceinline__ float query_factor(const uint32_t (&q)[W]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int k = 0; k < W; ++k) top = max(top, max(q[k] & 0x7fffu, (q[k] >> 16) & 0x7fffu));
-  return top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : exponent(min(253, 268 - int(top >> 7)));
 }
 
 // One piece of work: two tiles of a key head's rows over one run of their key tiles.
@@ -329,10 +342,114 @@ __device__ __forceinline__ AttendItem attend_item(const AttendTcParams& p, const
   return w;
 }
 
+// Eight values of row `row` from column c on, as fp32.
+template <int D, int KV>
+__device__ __forceinline__ void load8(const void* x, const float* scales, int64_t row, int c, float (&v)[8]) {
+  if constexpr (KV == kKvPagedE4m3) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(x) + row * D + c));
+    const float f = __ldg(scales + row);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t two = e4m3x2_to_bf16x2((k < 2 ? w.x : w.y) >> (16 * (k & 1)));
+      v[2 * k] = bf16_lo(two) * f;
+      v[2 * k + 1] = bf16_hi(two) * f;
+    }
+  } else {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(x) + row * D + c));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = bf16_lo(u[k]);
+      v[2 * k + 1] = bf16_hi(u[k]);
+    }
+  }
+}
+
+// Rows whose O holds something that is no finite number although their sum is one: a value that the
+// row does not see may have got into it, since the product multiplies it by a weight of zero. If a
+// tile that the rows see a part of holds such a value, those columns are summed again over the visible
+// keys alone. Called by a warp, one row per lane (token < 0: nothing odd in it); out of line, for the others.
+template <int D, int KV>
+__device__ __noinline__ void mend_rows(const AttendTcParams& p, const ItemWalk item, int g, int token, size_t row, float m,
+                                       float l) {
+  const int lane = threadIdx.x & 31;
+  const AttendItem w = attend_item<KV>(p, item);
+  const Sight mine = g ? w.see[1] : w.see[0];
+  auto row_of = [&](int j) -> int64_t {
+    if constexpr (KV == kKvPlain) return int64_t(w.bh) * p.N + j;
+    const int page = p.pages.table[size_t(w.b) * p.pages.max_pages + (j >> p.pages.log_page)];
+    if (page < 0 || page >= p.pages.num_pages) return -1;
+    return ((int64_t(page) * p.Hkv + w.hk) << p.pages.log_page) + (j & ((1 << p.pages.log_page) - 1));
+  };
+  bool spread = false;
+#pragma unroll 1
+  for (int i = w.tiles.from; i < w.tiles.to; ++i) {
+    const int j0 = w.tiles.key(i);
+    if (!mine.any(j0) || mine.all(p.win, j0, w.n)) continue;
+#pragma unroll 1
+    for (int j = j0 + lane; j < min(j0 + 128, w.n); j += 32) {
+      // pages that no row sees are not looked up: their entries may hold anything
+      if (KV != kKvPlain && !(j < w.both.sk || (j >= w.both.lo && j < w.both.hi))) continue;
+      const int64_t at = row_of(j);
+      if (at < 0) continue;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 8) {
+        float v[8];
+        load8<D, KV>(p.pages.V, p.pages.vs, at, c, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) spread |= !(fabsf(v[k]) < INFINITY);
+      }
+    }
+  }
+  if (!__any_sync(0xffffffffu, spread) || token < 0) return;
+  const int pos = w.n - w.nq + (g ? w.t0[1] : w.t0[0]) + token;
+  const int z = min(w.n - 1, pos + p.win.right), a = max(0, pos - p.win.left);
+  const float inv = 1.f / l;
+  const size_t to = size_t(w.split) * size_t(p.B) * p.Hq * p.N + row;
+  float acc[D];
+#pragma unroll 1
+  for (int c = 0; c < D; ++c) acc[c] = 0.f;
+#pragma unroll 1
+  for (int i = w.tiles.from; i < w.tiles.to; ++i) {
+    const int j0 = w.tiles.key(i);
+#pragma unroll 1
+    for (int j = j0; j < j0 + 128 && j <= z; ++j) {
+      if (j < a && j >= p.win.sinks) continue;
+      const int64_t at = row_of(j);
+      if (at < 0) continue;
+      float s = 0.f, x[8], y[8];
+#pragma unroll 1
+      for (int c = 0; c < D; c += 8) {
+        load8<D, kKvPlain>(p.Q, nullptr, int64_t(row), c, x);
+        load8<D, KV>(p.pages.K, p.pages.ks, at, c, y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = fmaf(x[k], y[k], s);
+      }
+      const float e = tc::ex2(fmaf(s, p.scale * 1.4426950408889634f, -m));
+#pragma unroll 1
+      for (int c = 0; c < D; c += 8) {
+        load8<D, KV>(p.pages.V, p.pages.vs, at, c, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[c + k] = fmaf(e, x[k], acc[c + k]);
+      }
+    }
+  }
+#pragma unroll 1
+  for (int c = 0; c < D; ++c) {
+    if (p.splits > 1) {
+      float* x = p.part + to * D + c;
+      if (!(fabsf(*x) < INFINITY)) *x = acc[c] * inv;
+    } else {
+      bf16* x = p.O + row * D + c;
+      if (!(fabsf(__bfloat162float(*x)) < INFINITY)) *x = __float2bfloat16(acc[c] * inv);
+    }
+  }
+}
+
 template <int D, int KV>
 __global__ void __launch_bounds__(384, 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const AttendTcParams p) {
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttendTcParams p) {
   using C = AttendTcCfg<D, KV>;
   using namespace tc;
   extern __shared__ __align__(16) uint8_t attend_smem[];
@@ -340,6 +457,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const uint32_t base_u = (raw_u + 1023u) & ~1023u;
   uint8_t* base = attend_smem + (base_u - raw_u);
   volatile int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC) + 1;
+  uint32_t* held_mask = reinterpret_cast<uint32_t*>(base + C::OFF_HELD);
   const uint32_t bar0 = base_u + C::OFF_BAR;
 #define ABAR(i) (bar0 + 8u * uint32_t(i))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -397,33 +515,38 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       for (int i = w.tiles.from; i < w.tiles.to && ok; ++i) {
         const int j0 = w.tiles.key(i);
         const int page = __shfl_sync(0xffffffffu, ahead, lane & (per - 1));
-        const int held = __popc(__ballot_sync(0xffffffffu, ahead >= 0));
+        const uint32_t held = __ballot_sync(0xffffffffu, ahead >= 0);
         ahead = page_at(i + 1);
         for (int kv = 0; kv < 2 && ok; ++kv, ++use) {
           const int s = use % NL;
           ok = __all_sync(0xffffffffu, wait_bounded(ABAR((C::CODES ? C::B_LEMPTY : C::B_EMPTY) + s), ((use / NL) & 1) ^ 1, abort_flag));
           if (!ok) break;
           const uint32_t dst = base_u + (C::CODES ? C::OFF_CODES + s * C::LAND : C::OFF_RING + s * C::TILE);
+          const uint32_t bar = ABAR((C::CODES || (KV == kKvPaged && kv) ? C::B_LAND : C::B_FULL) + s);
           if constexpr (KV == kKvPlain) {
-            if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_FULL + s), C::TILE);
+            if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE);
             __syncwarp();
-            if (lane * 64 < D)
-              tma_load_3d(dst + lane * 16384, kv ? &tmV : &tmK, ABAR(C::B_FULL + s), lane * 64, j0, w.bh);
+            if (lane * 64 < D) tma_load_3d(dst + lane * 16384, kv ? &tmV : &tmK, bar, lane * 64, j0, w.bh);
           } else {
-            if (lane == 0) mbar_arrive_expect_tx(ABAR(C::B_LAND + s), held * size * D * (C::CODES ? 1 : 2));
+            if (lane == 0) {
+              if (kv == 0) held_mask[(use >> 1) % C::kHeld] = held;
+              mbar_arrive_expect_tx(bar, __popc(held) * size * D * (C::CODES ? 1 : 2));
+            }
             __syncwarp();
             const int q = lane & (per - 1), panel = lane / per;  // whole rows of codes are one panel
             if (page >= 0 && panel < (C::CODES ? 1 : D / 64))
-              tma_load_3d(dst + (C::CODES ? q * size * D : panel * 16384 + q * size * 128), kv ? &tmV : &tmK,
-                          ABAR(C::B_LAND + s), panel * 64, 0, page * p.Hkv + w.hk);
+              tma_load_3d(dst + (C::CODES ? q * size * D : panel * 16384 + q * size * 128), kv ? &tmV : &tmK, bar,
+                          panel * 64, 0, page * p.Hkv + w.hk);
           }
         }
       }
     }
     // no copy may still be in flight when the CTA exits
-    constexpr int landed = KV == kKvPlain ? C::B_FULL : C::B_LAND;
     if (lane == 0)
-      for (int u = use > NL ? use - NL : 0; u < use; ++u) wait_drain(ABAR(landed + u % NL), (u / NL) & 1);
+      for (int u = use > NL ? use - NL : 0; u < use; ++u) {
+        if (KV == kKvPaged && (u & 1)) wait_drain(ABAR(C::B_LAND + u % NL), landed_parity<NL>(u));
+        else wait_drain(ABAR((C::CODES ? C::B_LAND : C::B_FULL) + u % NL), (u / NL) & 1);
+      }
   } else if (warp == 1) {
     // ------------------------------------------------------------- products
     constexpr uint32_t idS = idesc_bf16(128, 128, false), idO = idesc_bf16(128, D, true);
@@ -564,13 +687,13 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const uint32_t at_lo = (c0 ^ (r0 & 7)) << 4, at_hi = ((c0 + 1) ^ (r0 & 7)) << 4;
         for (int u = use; u < use + 2 * count; ++u) {
           const int sl = u % C::NL, s = u % C::NS, j0 = w.tiles.key(w.tiles.from + ((u - use) >> 1));
-          const uint32_t held = held_pages(p.pages, w.b, w.both, j0, lane);
-          const bool inner = (j0 + 128 <= w.both.sk || (j0 >= w.both.lo && j0 + 128 <= w.both.hi)) &&
-                             held == (1u << (128 >> p.pages.log_page)) - 1u;
           ok = wait_bounded(ABAR(C::B_EMPTY + s), ((u / C::NS) & 1) ^ 1, abort_flag) &&
                wait_bounded(ABAR(C::B_LAND + sl), (u / C::NL) & 1, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          const uint32_t held = held_mask[(u >> 1) % C::kHeld];
+          const bool inner = (j0 + 128 <= w.both.sk || (j0 >= w.both.lo && j0 + 128 <= w.both.hi)) &&
+                             held == (1u << (128 >> p.pages.log_page)) - 1u;
           const uint8_t* src = base + from + sl * C::LAND;
           uint8_t* dst = base + to + s * C::TILE;
 #pragma unroll 4
@@ -594,14 +717,14 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
       } else if constexpr (KV == kKvPaged) {
         if (warp == 2) {
-          for (int u = use; u < use + 2 * count; ++u) {
+          for (int u = use + 1; u < use + 2 * count; u += 2) {
             const int s = u % C::NS, j0 = w.tiles.key(w.tiles.from + ((u - use) >> 1));
-            ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_LAND + s), (u / C::NS) & 1, abort_flag));
+            ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_LAND + s), landed_parity<C::NS>(u), abort_flag));
             if (!ok) break;
+            const uint32_t held = held_mask[(u >> 1) % C::kHeld];
             // values of rows that the window's or the sequence's edge leaves out
             const bool inner = j0 + 128 <= w.both.sk || (j0 >= w.both.lo && j0 + 128 <= w.both.hi);
-            const uint32_t held = (u - use) & 1 ? held_pages(p.pages, w.b, w.both, j0, lane) : 0u;
-            if (((u - use) & 1) && !(inner && held == (1u << (128 >> p.pages.log_page)) - 1u)) {
+            if (!(inner && held == (1u << (128 >> p.pages.log_page)) - 1u)) {
               for (int r = lane; r < 128; r += 32) {
                 const int j = j0 + r;
                 const bool in = ((held >> (r >> p.pages.log_page)) & 1u) && (j < w.both.sk || (j >= w.both.lo && j < w.both.hi));
@@ -632,6 +755,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint32_t s_addr = tmem + lrow + C::S_COL + g * 128, o_addr = tmem + lrow + C::O_COL + g * D;
     const float sl2 = p.scale * 1.4426950408889634f;
     float* scales = reinterpret_cast<float*>(base + C::OFF_SCALE) + (C::CODES ? (warp - 4) * 256 : 0);
+    const uint32_t full_mask = (1u << (128 >> p.pages.log_page)) - 1u;
     bool ok = true;
     uint32_t n_s = 0, n_o = 0;
     int use = 0;  // stage uses of the items before
@@ -670,11 +794,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       for (int i = w.tiles.from; i < w.tiles.to; ++i) {
         const int j0 = w.tiles.key(i);
         if (!mine.any(j0)) continue;
-        uint32_t held = 0xffu;
-        if constexpr (KV != kKvPlain) held = held_pages(p.pages, w.b, mine, j0, lane);
-        const bool whole = j0 + 127 <= mine.p0 + p.win.right && j0 + 128 <= w.n &&
-                           (j0 >= mine.p1 - p.win.left || j0 + 128 <= p.win.sinks) &&
-                           (KV == kKvPlain || held == (1u << (128 >> p.pages.log_page)) - 1u);
+        const bool seen = mine.all(p.win, j0, w.n);
         if constexpr (C::CODES) {
           __syncwarp();  // the previous tile's scales have been read
           reinterpret_cast<float4*>(scales)[lane] = next_k;
@@ -687,6 +807,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (!ok) break;
         n_s ^= 1u;
         tc_fence_after();
+        uint32_t held = 0xffu;
+        if constexpr (KV != kKvPlain) held = held_mask[((use >> 1) + i - w.tiles.from) % C::kHeld];
+        const bool whole = seen && (KV == kKvPlain || held == full_mask);
         uint32_t sc[128];
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) tmem_ld16(s_addr + ch * 16, *reinterpret_cast<uint32_t(*)[16]>(&sc[ch * 16]));
@@ -774,6 +897,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const float inv = l != 0.f ? 1.f / l : 0.f;  // l is NaN if a score was
       const bool split_out = p.splits > 1;
       const size_t to = size_t(w.split) * size_t(p.B) * p.Hq * p.N + row;
+      float zero[2] = {0.f, 0.f};  // NaN once a value is no finite number
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
         __syncwarp();
@@ -787,6 +911,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[0][k] = o[1][k] = 0u;
         }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          zero[0] = fmaf(__uint_as_float(o[0][k]), 0.f, zero[0]);
+          zero[1] = fmaf(__uint_as_float(o[1][k]), 0.f, zero[1]);
+        }
         if (split_out) store_part32(p.part + ch * 32, real ? int64_t(to) * D : -1, o, inv);
         else store_rows32(p.O + ch * 32, real ? int64_t(row) * D : -1, o, inv);
       }
@@ -796,6 +925,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (split_out) p.part_lse[to] = lg;
         else if (p.lse) p.lse[row] = lg * 0.6931471805599453f;
       }
+      const bool odd = real && done && zero[0] + zero[1] != 0.f && l == l;
+      if (__any_sync(0xffffffffu, odd)) mend_rows<D, KV>(p, at, g, odd ? my_token : -1, row, m, l);
       tc_fence_before();
       use += 2 * (w.tiles.to - w.tiles.from);
     }

@@ -470,6 +470,67 @@ attend_token_kernel(const AttendTokenParams p) {
             m[h][e] = top;
           }
       }
+      // Tokens that do not all see the step: a value that is no finite number would reach them through
+      // a weight of zero. It leaves the products, and joins O of the rows that see it here.
+      if (!whole && s.see.p0 != s.see.p1) {
+        auto sees = [&](int j, int h, int e) { return j <= z[h][e] && (j >= a[h][e] || j < p.win.sinks); };
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          if constexpr (E4M3) {
+            odd |= !(fabsf(vs[i][0]) < INFINITY) || !(fabsf(vs[i][1]) < INFINITY);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int x = 0; x < VW; x += 4)
+                odd |= any_not_finite(make_uint4(vr[i][e][x], vr[i][e][x + 1], vr[i][e][x + 2], vr[i][e][x + 3]));
+          }
+        }
+        if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            if constexpr (E4M3) {  // NaN in every column
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const bool bad = !(fabsf(vs[i][t]) < INFINITY);
+                if (bad) vs[i][t] = 0.f;
+#pragma unroll
+                for (int h = 0; h < NR; ++h)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const uint32_t lanes = __ballot_sync(0xffffffffu, bad && sees(j0 + i * 16 + 8 * t + g, h, e));
+                    if (!(lanes & (0x11111111u << q))) continue;
+#pragma unroll
+                    for (int x = 0; x < MT; ++x) o[h][x][e] = o[h][x][e + 2] = __uint_as_float(0x7fc00000u);
+                  }
+              }
+            } else {
+#pragma unroll 1
+              for (int from = 0; from < 4; ++from)  // the lanes of the quad hold four keys each
+#pragma unroll
+                for (int e4 = 0; e4 < 4; ++e4)
+#pragma unroll
+                  for (int x = 0; x < VW; ++x) {
+                    const uint32_t v = __shfl_sync(0xffffffffu, vr[i][e4][x], (lane & ~3) + from);
+                    const int j = j0 + i * 16 + 2 * from + (e4 & 1) + (e4 >> 1) * 8;
+#pragma unroll
+                    for (int h = 0; h < NR; ++h)
+#pragma unroll
+                      for (int e = 0; e < 2; ++e)
+                        if (sees(j, h, e)) {
+                          o[h][x][e] += not_finite_lo(v);
+                          o[h][x][e + 2] += not_finite_hi(v);
+                        }
+                  }
+#pragma unroll
+              for (int e4 = 0; e4 < 4; ++e4)
+#pragma unroll
+                for (int x = 0; x < VW; ++x) vr[i][e4][x] = finite_or_zero(vr[i][e4][x]);
+            }
+          }
+        }
+      }
       bool wide = false;
       float tm[NR][2];
 #pragma unroll

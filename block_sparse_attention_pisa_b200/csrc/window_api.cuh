@@ -162,6 +162,8 @@ pisa_status_t launch_attend_tc(pisa::AttendTcParams p, const void* K, const void
   if constexpr (KV == pisa::kKvPlain) {
     PISA_TRY(make_map(&mK, K, D, uint64_t(p.N), uint64_t(p.B) * p.Hkv, 128));
     PISA_TRY(make_map(&mV, V, D, uint64_t(p.N), uint64_t(p.B) * p.Hkv, 128));
+    p.pages.K = K;
+    p.pages.V = V;
   } else if constexpr (KV == pisa::kKvPaged) {
     PISA_TRY(make_map(&mK, K, D, uint64_t(page), uint64_t(num_pages) * p.Hkv, uint32_t(page)));
     PISA_TRY(make_map(&mV, V, D, uint64_t(page), uint64_t(num_pages) * p.Hkv, uint32_t(page)));

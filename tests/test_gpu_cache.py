@@ -461,3 +461,56 @@ def test_two_streams_at_once():
                 got.append(P.paged_attention(q, cache, table, n))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for x, y in zip(want, got) for a, b in zip(x, y))
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")], ids=["nan", "inf"])
+@pytest.mark.parametrize("N,Hq,d,mask", [
+    (2, 4, 64, dict(left=-1, right=0, sinks=0)),
+    (8, 4, 128, dict(left=40, right=0, sinks=7)),
+    (5, 6, 64, dict(left=3, right=1, sinks=0)),
+    (90, 2, 128, dict(left=-1, right=0, sinks=0)),
+    (90, 6, 64, dict(left=33, right=10, sinks=50)),
+])
+def test_a_token_that_is_not_finite_reaches_the_rows_that_see_it(dtype, what, N, Hq, d, mask):
+    """A value (in 8 bits its whole row) reaches the rows that see it; the others hold what they held
+    (rows that share a tile with it sum again, without rounding the weights: 3 u max|v|). A key
+    changes no bit of a row that does not see it. Tokens of the chunk, and older ones."""
+    Hkv, page, lens = 2, 16, [400, 210]
+    cache, table = filled(lens, Hkv, page, d, dtype, seed=8)
+    Q = randn(2, Hq, N, d, seed=80)
+    O, lse = P.paged_attention(Q, cache, table, ints(lens), **mask)
+    top = float(np.nanmax(np.abs(values(cache)[1])))
+    G, b, hk = Hq // Hkv, 1, 1
+    left, right, sinks = (lens[b] if v < 0 else v for v in mask.values())
+    p = np.arange(N) + lens[b] - N
+    for at in (lens[b] - 1, lens[b] - 2, lens[b] - N, lens[b] - N - 2, 4):
+        see = torch.from_numpy((at <= p + right) & ((at >= p - left) | (at < sinks))).cuda()
+        i, r = int(table[b, at // page]), at % page
+        for key in (False, True):
+            t = cache.K if key else cache.V
+            if dtype == E4M3:
+                t = cache.k_scale if key else cache.v_scale
+            old = t[i, hk, r].clone()
+            if dtype == E4M3:
+                t[i, hk, r] = float("nan")
+            else:
+                t[i, hk, r, 5] = what
+            got, glse = P.paged_attention(Q, cache, table, ints(lens), **mask)
+            t[i, hk, r] = old
+            want = O.clone()
+            mine = want[b, hk * G:(hk + 1) * G]
+            if key:
+                assert torch.equal(got[b, :, ~see], O[b, :, ~see]) and torch.equal(glse[b, :, ~see], lse[b, :, ~see])
+                assert torch.equal(got[b, :hk * G], O[b, :hk * G]) and torch.equal(got[0], O[0])
+                continue
+            assert torch.equal(glse, lse)
+            cols = slice(None) if dtype == E4M3 else slice(5, 6)
+            mine[:, see, cols] = float("nan") if dtype == E4M3 else what
+            assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+            have = got[b, hk * G:(hk + 1) * G]
+            off = (have.float() - mine.float())[:, ~see, cols].abs()
+            assert not off.numel() or float(off.max()) <= T.SLACK * 3 * T.U * top
+            have[..., cols] = mine[..., cols]
+            assert torch.equal(got.nan_to_num(), want.nan_to_num())
+    P.device_error()

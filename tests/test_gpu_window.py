@@ -264,3 +264,39 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")], ids=["nan", "inf", "-inf"])
+def test_a_value_that_is_not_finite_reaches_the_rows_that_see_it(d, what):
+    """One element of one value changes its column alone: there the rows that see it hold it, the
+    others what they held (a row that shares a tile with it sums the column again, with weights that
+    are not rounded: off by a rounding of p and one of either O, 3 u max|v|). A key changes no bit of
+    the rows that do not see it. Tiles that every row sees whole and partly seen ones."""
+    B, Hq, Hkv, N = 2, 6, 2, 700
+    Q, K, V, _ = make(B, Hq, Hkv, N, d, seed=51)
+    p, j = np.arange(N)[:, None], np.arange(N)[None]
+    for left, right, sinks in ((-1, 0, 0), (90, 0, 5), (-1, -1, 0), (20, 200, 0)):
+        mask = dict(left=left, right=right, sinks=sinks)
+        see = (j <= p + (N if right < 0 else right)) & ((j >= p - (N if left < 0 else left)) | (j < sinks))
+        O, lse = P.window_attention(Q, K, V, **mask)
+        for at in (3, 130, 255, 256, 500, 699):
+            c = at % d
+            rows = torch.from_numpy(see[:, at]).cuda()
+            bad = V.clone()
+            bad[1, 1, at, c] = what
+            got, glse = P.window_attention(Q, K, bad, **mask)
+            assert torch.equal(glse, lse)
+            want = O.clone()
+            want[1, 3:, rows, c] = what
+            assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+            off = (got.float() - O.float())[1, 3:, ~rows, c].abs()
+            assert not off.numel() or float(off.max()) <= T.SLACK * 3 * T.U * float(V[1, 1, :, c].abs().max())
+            got[1, 3:, :, c] = want[1, 3:, :, c]
+            assert torch.equal(got.nan_to_num(), want.nan_to_num())
+            bad = K.clone()
+            bad[1, 1, at] = what
+            got, glse = P.window_attention(Q, bad, V, **mask)
+            want = O.clone()
+            assert torch.equal(got[:, :, ~rows], O[:, :, ~rows]) and torch.equal(glse[:, :, ~rows], lse[:, :, ~rows])
+            assert torch.equal(got[:, :3], O[:, :3]) and torch.equal(got[0], O[0])
