@@ -8,6 +8,11 @@ stream. Every step of the computation runs in the library's CUDA kernels;
 there is no CPU or PyTorch fallback -- if the library is missing or the
 device is not a B200 the calls raise.
 
+Besides the block-sparse path: attention under a token-exact window with its
+gradient (``window_attention``, ``window_attention_backward``), and a paged cache
+with the attention that reads it (``paged_cache``, ``cache_write``,
+``cache_read``, ``paged_attention``).
+
 Method: "PISA: Piecewise Sparse Attention Is Wiser for Efficient Diffusion
 Transformers" (explainer of arXiv 2602.01077 on gist.science), technical
 summary section 2.

@@ -91,6 +91,7 @@ attend_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   uint8_t* base = attend_dq_smem + (base_u - raw_u);
   volatile int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC) + 1;
   const uint32_t bar0 = base_u + C::OFF_BAR;
+  asm volatile("griddepcontrol.launch_dependents;");
 #define ABAR(i) (bar0 + 8u * uint32_t(i))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -410,6 +411,7 @@ attend_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   int* misc = reinterpret_cast<int*>(base + C::OFF_MISC);
   volatile int* abort_flag = misc + 1;
   const uint32_t bar0 = base_u + C::OFF_BAR;
+  asm volatile("griddepcontrol.launch_dependents;");
 #define ABAR(i) (bar0 + 8u * uint32_t(i))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv, BH = p.B * p.Hkv;
@@ -445,6 +447,8 @@ attend_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       misc[5] = f.slot;
     }
   }
+  // the setup ran beside the dQ kernel's last blocks; delta is that kernel's
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uint32_t(misc[0]);
@@ -647,8 +651,12 @@ constexpr int kJoinSlices = 16;
 template <int D>
 __global__ void __launch_bounds__(256) attend_dkv_join_kernel(const AttendGradParams p) {
   const int kts = (p.N + 127) / 128, kt = blockIdx.x / kJoinSlices % kts, bh = blockIdx.x / kJoinSlices / kts;
-  if (query_runs((p.Hq / p.Hkv) * QueryRange(p.win, kt, p.N).count, p.run) <= 1) return;
-  const RunAt f = find_run(p, -1, kt);  // every warp finds the same
+  const bool cut = query_runs((p.Hq / p.Hkv) * QueryRange(p.win, kt, p.N).count, p.run) > 1;
+  RunAt f{};
+  if (cut) f = find_run(p, -1, kt);  // every warp finds the same
+  // every block waits, so that this grid does not end before the one it depends on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!cut) return;
   constexpr int ALL = 2 * 128 * D, SLICE = ALL / kJoinSlices;
   const float* src = p.part + (size_t(bh) * p.slots + f.slot) * ALL;
   for (int e = blockIdx.x % kJoinSlices * SLICE + threadIdx.x * 4, end = (blockIdx.x % kJoinSlices + 1) * SLICE; e < end; e += 1024) {

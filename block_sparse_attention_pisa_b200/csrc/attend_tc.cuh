@@ -457,6 +457,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const uint32_t base_u = (raw_u + 1023u) & ~1023u;
   uint8_t* base = attend_smem + (base_u - raw_u);
   volatile int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC) + 1;
+  asm volatile("griddepcontrol.launch_dependents;");
   uint32_t* held_mask = reinterpret_cast<uint32_t*>(base + C::OFF_HELD);
   const uint32_t bar0 = base_u + C::OFF_BAR;
 #define ABAR(i) (bar0 + 8u * uint32_t(i))
@@ -944,6 +945,8 @@ template <int D>
 __global__ void __launch_bounds__(128) attend_join_kernel(const AttendTcParams p, int paged) {
   const int lane = threadIdx.x & 31;
   const int64_t rows = int64_t(p.B) * p.Hq * p.N, row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  // every block waits, so that this grid does not end before the one it depends on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows) return;
   if (paged) {
     const int b = int(row / (int64_t(p.Hq) * p.N)), t = int(row % p.N);

@@ -153,6 +153,26 @@ size_t attend_workspace(const pisa::AttendTcParams& p, int d) {
   return p.splits > 1 ? size_t(p.splits) * p.B * p.Hq * p.N * (size_t(d) + 1) * 4 : 0;
 }
 
+// A kernel whose blocks start as the last ones of the kernel before it run (which lets them with
+// griddepcontrol.launch_dependents); they set up and wait (griddepcontrol.wait) for it to end.
+template <class... Args>
+pisa_status_t launch_behind(void (*kernel)(Args...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
+                            const char* name, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) return fail(PISA_ERR_CUDA, "%s launch: %s", name, cudaGetErrorString(e));
+  return check_launch(name);
+}
+
 template <int D, int KV>
 pisa_status_t launch_attend_tc(pisa::AttendTcParams p, const void* K, const void* V, int page, int num_pages,
                                void* workspace, cudaStream_t st) {
@@ -181,8 +201,8 @@ pisa_status_t launch_attend_tc(pisa::AttendTcParams p, const void* K, const void
   k<<<unsigned(p.items < kSms ? p.items : kSms), C::kThreads, C::SMEM, st>>>(mQ, mK, mV, p);
   PISA_TRY(check_launch("attend_tc_kernel"));
   if (p.splits > 1) {
-    pisa::attend_join_kernel<D><<<unsigned((rows + 3) / 4), 128, 0, st>>>(p, KV != pisa::kKvPlain);
-    PISA_TRY(check_launch("attend_join_kernel"));
+    PISA_TRY(launch_behind(pisa::attend_join_kernel<D>, unsigned((rows + 3) / 4), 128, 0, st, "attend_join_kernel", p,
+                           int(KV != pisa::kKvPlain)));
   }
   return ok();
 }
@@ -226,19 +246,9 @@ pisa_status_t launch_token(const pisa::AttendTcParams& a, int ctas, void* worksp
   auto k = rows > 8 ? pisa::attend_token_kernel<D, E4M3, 2> : pisa::attend_token_kernel<D, E4M3, 1>;
   k<<<unsigned(ctas), 32 * pisa::kTokenWarps, 0, st>>>(p);
   PISA_TRY(check_launch("attend_token_kernel"));
-  // the join's blocks start while the pieces are still being computed, and wait for them
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(a.B * a.Hkv * rows));
-  cfg.blockDim = dim3(32 * pisa::kTokenWarps);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, pisa::attend_token_join_kernel<D>, p);
-  if (e != cudaSuccess) return fail(PISA_ERR_CUDA, "attend_token_join_kernel launch: %s", cudaGetErrorString(e));
-  return check_launch("attend_token_join_kernel");
+  PISA_TRY(launch_behind(pisa::attend_token_join_kernel<D>, unsigned(a.B * a.Hkv * rows), 32 * pisa::kTokenWarps, 0, st,
+                         "attend_token_join_kernel", p));
+  return ok();
 }
 
 // How the key tiles of the gradient are cut into runs of query tiles: as if two CTAs per SM shared
@@ -288,12 +298,11 @@ pisa_status_t launch_grad(pisa::AttendGradParams p, const GradPlan& g, const voi
   const unsigned row_tiles = unsigned(p.rt.parts) * unsigned((p.N + p.rt.tokens - 1) / p.rt.tokens);
   kq<<<row_tiles * unsigned(heads), Cq::kThreads, Cq::SMEM, st>>>(rQ, rG, rO, mK, mV, p);
   PISA_TRY(check_launch("attend_dq_kernel"));
-  kk<<<unsigned(g.runs) * unsigned(heads), Ck::kThreads, Ck::SMEM, st>>>(mK, mV, mQ, mG, p);
-  PISA_TRY(check_launch("attend_dkv_kernel"));
-  if (g.slots > 0) {
-    pisa::attend_dkv_join_kernel<D><<<unsigned((N + 127) / 128 * heads) * pisa::kJoinSlices, 256, 0, st>>>(p);
-    PISA_TRY(check_launch("attend_dkv_join_kernel"));
-  }
+  PISA_TRY(launch_behind(kk, unsigned(g.runs) * unsigned(heads), Ck::kThreads, Ck::SMEM, st, "attend_dkv_kernel", mK, mV, mQ,
+                         mG, p));
+  if (g.slots > 0)
+    PISA_TRY(launch_behind(pisa::attend_dkv_join_kernel<D>, unsigned((N + 127) / 128 * heads) * pisa::kJoinSlices, 256, 0, st,
+                           "attend_dkv_join_kernel", p));
   return ok();
 }
 
