@@ -404,7 +404,7 @@ __device__ __noinline__ void mend_rows(const AttendTcParams& p, const ItemWalk i
   if (!__any_sync(0xffffffffu, spread) || token < 0) return;
   const int pos = w.n - w.nq + (g ? w.t0[1] : w.t0[0]) + token;
   const int z = min(w.n - 1, pos + p.win.right), a = max(0, pos - p.win.left);
-  const float inv = 1.f / l;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
   const size_t to = size_t(w.split) * size_t(p.B) * p.Hq * p.N + row;
   float acc[D];
 #pragma unroll 1

@@ -514,3 +514,19 @@ def test_a_token_that_is_not_finite_reaches_the_rows_that_see_it(dtype, what, N,
             have[..., cols] = mine[..., cols]
             assert torch.equal(got.nan_to_num(), want.nan_to_num())
     P.device_error()
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("N,Hq", [(7, 2), (90, 2), (90, 6)])
+def test_rows_that_see_nothing_beside_rows_that_see_a_nan(dtype, N, Hq):
+    """More new tokens than the sequence holds: the first ones have negative positions and see
+    nothing, whatever the values that the others of their tile see."""
+    Hkv, page, d = 2, 16, 64
+    lens = [N - 4, 300]
+    cache, table = filled(lens, Hkv, page, d, dtype, seed=9)
+    Q = randn(2, Hq, N, d, seed=81)
+    (cache.V if dtype == BF16 else cache.v_scale)[int(table[0, 0]), :, 1] = float("nan")
+    O, lse = P.paged_attention(Q, cache, table, ints(lens))
+    assert (O[0, :, :4] == 0).all() and (lse[0, :, :4] == float("-inf")).all()
+    assert torch.isfinite(O[0, :, 4].float()).all() and torch.isnan(O[0, :, 5:].float()).all()
+    assert torch.isfinite(O[1].float()).all() and torch.isfinite(lse[0, :, 4:]).all() and torch.isfinite(lse[1]).all()
