@@ -940,11 +940,14 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #undef ABAR
 }
 
-// Joins the runs of a row: weights 2^(lse_s - max), in run order. One warp per row.
+// Joins the runs of a row: weights 2^(lse_s - max), in run order. D / 4 lanes per row, whose loads of
+// several runs are in flight at once. Bound by memory (the partial sums are read once).
+constexpr int kJoinThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(128) attend_join_kernel(const AttendTcParams p, int paged) {
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = int64_t(p.B) * p.Hq * p.N, row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendTcParams p, int paged) {
+  constexpr int LANES = D / 4, ROWS = kJoinThreads / LANES;
+  const int64_t rows = int64_t(p.B) * p.Hq * p.N, row = int64_t(blockIdx.x) * ROWS + threadIdx.x / LANES;
+  const int c = threadIdx.x % LANES * 4;
   // every block waits, so that this grid does not end before the one it depends on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows) return;
@@ -953,23 +956,21 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendTcParams p
     if (t >= q_len_of(p.pages, b, p.N)) return;
   }
   float m = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.part_lse[s * rows + row]);
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, __ldg(p.part_lse + s * rows + row));
   const float m0 = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float w = tc::ex2(p.part_lse[s * rows + row] - m0);
-    if (w == 0.f) continue;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {  // a run that saw nothing holds zeros
+    const float w = tc::ex2(__ldg(p.part_lse + s * rows + row) - m0);
+    const float4 x = __ldcs(reinterpret_cast<const float4*>(p.part + (s * rows + row) * D + c));
     l += w;
-    const float* src = p.part + (s * rows + row) * D;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = fmaf(w, src[i * 32 + lane], o[i]);
+    o = make_float4(fmaf(w, x.x, o.x), fmaf(w, x.y, o.y), fmaf(w, x.z, o.z), fmaf(w, x.w, o.w));
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) p.O[row * D + i * 32 + lane] = __float2bfloat16(o[i] * inv);
-  if (lane == 0 && p.lse) p.lse[row] = l != 0.f ? (m0 + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+  *reinterpret_cast<uint2*>(p.O + row * D + c) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (c == 0 && p.lse) p.lse[row] = l != 0.f ? (m0 + __log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace pisa

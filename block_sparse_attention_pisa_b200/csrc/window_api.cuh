@@ -201,8 +201,9 @@ pisa_status_t launch_attend_tc(pisa::AttendTcParams p, const void* K, const void
   k<<<unsigned(p.items < kSms ? p.items : kSms), C::kThreads, C::SMEM, st>>>(mQ, mK, mV, p);
   PISA_TRY(check_launch("attend_tc_kernel"));
   if (p.splits > 1) {
-    PISA_TRY(launch_behind(pisa::attend_join_kernel<D>, unsigned((rows + 3) / 4), 128, 0, st, "attend_join_kernel", p,
-                           int(KV != pisa::kKvPlain)));
+    constexpr int per = pisa::kJoinThreads / (D / 4);  // rows of a block
+    PISA_TRY(launch_behind(pisa::attend_join_kernel<D>, unsigned((rows + per - 1) / per), pisa::kJoinThreads, 0, st,
+                           "attend_join_kernel", p, int(KV != pisa::kKvPlain)));
   }
   return ok();
 }
