@@ -38,10 +38,13 @@
 // instruction, the pack to bf16 as long again, two fma and add per value), and then, of either group,
 // the chain "second half of P V, next Q K^T, its commit" that the other group only partly covers.
 // 2 x 24 heads of 4096 x 128, 512 keys to either side: 148 us, 0.65 PFLOP/s; 2 x 1024 tokens of 24
-// heads over a paged cache of 16 K, window 8192: 265 us, 0.78 PFLOP/s; D = 64 has the same softmax for
+// heads over a paged cache of 16 K, window 8192: 257 us, 0.81 PFLOP/s; D = 64 has the same softmax for
 // half the products. What was tried and measured slower: one 128-row tile with two score buffers;
 // two threads per row; a maximum guessed from the tile before; separate columns for P; packed fp32
-// pairs for the scaling; setmaxnreg (the roles that give registers away spill).
+// pairs for the scaling; setmaxnreg (the roles that give registers away spill); the last wave's pairs
+// cut in two (one tile takes as long as a pair: its own chain).
+// 8 bits, D = 64: 3 sequences of 333 tokens, 12 and 4 heads, 5 K keys: 67 us; without the scales (128 products and
+// 32 shared-memory loads of either kind per row and tile) 56, without the conversion 65.
 #pragma once
 
 #include "attention_tc.cuh"
@@ -238,6 +241,14 @@ __device__ __forceinline__ void fma2(float& x0, float& x1, float a, float b) {
       "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
       "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "+f"(x0), "+f"(x1)
+      : "f"(a), "f"(b));
+}
+// the fp32 values of two words, times a and b
+__device__ __forceinline__ void mul2(uint32_t& x0, uint32_t& x1, float a, float b) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+r"(x0), "+r"(x1)
       : "f"(a), "f"(b));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -820,10 +831,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             const float4 f = reinterpret_cast<const float4*>(scales)[k];
-            sc[4 * k] = __float_as_uint(__uint_as_float(sc[4 * k]) * f.x);
-            sc[4 * k + 1] = __float_as_uint(__uint_as_float(sc[4 * k + 1]) * f.y);
-            sc[4 * k + 2] = __float_as_uint(__uint_as_float(sc[4 * k + 2]) * f.z);
-            sc[4 * k + 3] = __float_as_uint(__uint_as_float(sc[4 * k + 3]) * f.w);
+            mul2(sc[4 * k], sc[4 * k + 1], f.x, f.y);
+            mul2(sc[4 * k + 2], sc[4 * k + 3], f.z, f.w);
           }
         }
         if (!whole) {
@@ -864,14 +873,17 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
           uint32_t pk[16];
+          float4 f;
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const float e0 = ex2(fmaf(__uint_as_float(sc[ch * 32 + 2 * k]), sl2, negm));
             const float e1 = ex2(fmaf(__uint_as_float(sc[ch * 32 + 2 * k + 1]), sl2, negm));
             sum[k & 3] += e0 + e1;
             if constexpr (C::CODES) {  // the value's scale may be NaN, or the weight huge beside it
-              const float2 f = reinterpret_cast<const float2*>(scales + 128)[ch * 16 + k];
-              pk[k] = pack_bf16x2(e0 * f.x, e1 * f.y);
+              if (k % 2 == 0) f = reinterpret_cast<const float4*>(scales + 128)[ch * 8 + k / 2];
+              uint32_t x0 = __float_as_uint(e0), x1 = __float_as_uint(e1);
+              mul2(x0, x1, k % 2 ? f.z : f.x, k % 2 ? f.w : f.y);
+              pk[k] = pack_bf16x2(__uint_as_float(x0), __uint_as_float(x1));
             } else {
               pk[k] = pack_bf16x2(e0, e1);
             }
