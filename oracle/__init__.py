@@ -20,6 +20,9 @@ function here is pinned by tests in ``tests/test_oracle_pins.py`` (brute force
 on tiny inputs, closed forms, reductions to textbook softmax attention,
 convergence rates, and an independent second formulation of the first-order
 term).
+
+``oracle.window`` is the oracle of the windowed attention, its gradient and the
+quantised cache, pinned by ``tests/test_window_oracle.py``.
 """
 from .pisa import (  # noqa: F401
     block_bounds,
