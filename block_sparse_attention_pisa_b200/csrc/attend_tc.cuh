@@ -417,6 +417,25 @@ __device__ __noinline__ void mend_rows(const AttendTcParams& p, const ItemWalk i
   const int z = min(w.n - 1, pos + p.win.right), a = max(0, pos - p.win.left);
   const float inv = l != 0.f ? 1.f / l : 0.f;
   const size_t to = size_t(w.split) * size_t(p.B) * p.Hq * p.N + row;
+  // a row that sees a key whose value is NaN throughout keeps its NaN: once a sequence is lost, all do
+#pragma unroll 1
+  for (int i = w.tiles.from; i < w.tiles.to; ++i) {
+    const int j0 = w.tiles.key(i);
+    if (!mine.any(j0) || mine.all(p.win, j0, w.n)) continue;
+#pragma unroll 1
+    for (int j = j0; j < j0 + 128 && j <= z; ++j) {
+      const int64_t at = j >= a || j < p.win.sinks ? row_of(j) : -1;
+      bool nan = at >= 0;
+#pragma unroll 1
+      for (int c = 0; nan && c < D; c += 8) {
+        float v[8];
+        load8<D, KV>(p.pages.V, p.pages.vs, at, c, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) nan = nan && v[k] != v[k];
+      }
+      if (nan) return;
+    }
+  }
   float acc[D];
 #pragma unroll 1
   for (int c = 0; c < D; ++c) acc[c] = 0.f;

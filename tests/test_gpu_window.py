@@ -300,3 +300,26 @@ def test_a_value_that_is_not_finite_reaches_the_rows_that_see_it(d, what):
             want = O.clone()
             assert torch.equal(got[:, :, ~rows], O[:, :, ~rows]) and torch.equal(glse[:, :, ~rows], lse[:, :, ~rows])
             assert torch.equal(got[:, :3], O[:, :3]) and torch.equal(got[0], O[0])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_sequence_that_is_lost_from_a_token_on(d):
+    """Keys and values are NaN (values: NaN and infinities in turn) from token 2900 on: rows before it
+    hold what they held, to the roundings of the rows that share a tile with it; the others are NaN."""
+    B, Hq, Hkv, N, at = 1, 4, 2, 4000, 2900
+    Q, K, V, _ = make(B, Hq, Hkv, N, d, seed=52)
+    for mask in (dict(left=-1, right=0), dict(left=700, right=0, sinks=9)):
+        O, _ = P.window_attention(Q, K, V, **mask)
+        for lose_keys in (False, True):
+            bad_k, bad_v = K.clone(), V.clone()
+            bad_v[:, :, at:] = float("nan")
+            bad_v[:, :, at::3, ::2] = float("inf")
+            if lose_keys:
+                bad_k[:, :, at:] = float("nan")
+            got, lse = P.window_attention(Q, bad_k, bad_v, **mask)
+            off = (got - O)[:, :, :at].float().abs()
+            assert float(off.max()) <= T.SLACK * 3 * T.U * float(V.abs().max())
+            assert not torch.isfinite(got[:, :, at:].float()).any()
+            assert torch.isfinite(lse[:, :, :at]).all()
+            assert bool(torch.isnan(lse[:, :, at:]).all()) == lose_keys
+    P.device_error()
