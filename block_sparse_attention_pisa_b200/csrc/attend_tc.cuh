@@ -43,8 +43,8 @@
 // two threads per row; a maximum guessed from the tile before; separate columns for P; packed fp32
 // pairs for the scaling; setmaxnreg (the roles that give registers away spill); the last wave's pairs
 // cut in two (one tile takes as long as a pair: its own chain).
-// 8 bits, D = 64: 3 sequences of 333 tokens, 12 and 4 heads, 5 K keys: 67 us; without the scales (128 products and
-// 32 shared-memory loads of either kind per row and tile) 56, without the conversion 65.
+// 8 bits, D = 64: 3 sequences of 333 tokens, 12 and 4 heads, 5 K keys: 67 us; without the scales (128
+// products and 32 shared-memory loads of either kind per row and tile) 56, without the conversion 65.
 #pragma once
 
 #include "attention_tc.cuh"
