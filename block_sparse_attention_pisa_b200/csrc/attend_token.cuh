@@ -495,6 +495,14 @@ attend_token_kernel(const AttendTokenParams p) {
               for (int t = 0; t < 2; ++t) {
                 const bool bad = !(fabsf(vs[i][t]) < INFINITY);
                 if (bad) vs[i][t] = 0.f;
+                // its codes may be NaN too: those of keys 2 q and 2 q + 1 (and 8 more) are this lane's,
+                // their scales lanes 8 q's and 8 q + 4's
+                const uint32_t rows = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+                for (int e2 = 0; e2 < 2; ++e2)
+                  if ((rows >> (8 * q + 4 * e2)) & 1u)
+#pragma unroll
+                    for (int x = 0; x < VW; ++x) vr[i][2 * t + e2][x] = 0u;
 #pragma unroll
                 for (int h = 0; h < NR; ++h)
 #pragma unroll

@@ -530,3 +530,48 @@ def test_rows_that_see_nothing_beside_rows_that_see_a_nan(dtype, N, Hq):
     assert (O[0, :, :4] == 0).all() and (lse[0, :, :4] == float("-inf")).all()
     assert torch.isfinite(O[0, :, 4].float()).all() and torch.isnan(O[0, :, 5:].float()).all()
     assert torch.isfinite(O[1].float()).all() and torch.isfinite(lse[0, :, 4:]).all() and torch.isfinite(lse[1]).all()
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")], ids=["nan", "inf"])
+@pytest.mark.parametrize("N,Hq,d,mask", [
+    (2, 4, 64, dict(left=-1, right=0, sinks=0)),
+    (3, 8, 128, dict(left=-1, right=0, sinks=0)),
+    (8, 4, 128, dict(left=40, right=0, sinks=7)),
+    (5, 6, 64, dict(left=3, right=1, sinks=0)),
+    (90, 2, 128, dict(left=-1, right=0, sinks=0)),
+    (90, 6, 64, dict(left=33, right=10, sinks=50)),
+])
+def test_a_lost_token_as_the_cache_holds_it(what, N, Hq, d, mask):
+    """8 bits: the row of a token that is not finite, written by cache_write (codes and scale are
+    both NaN then), reaches the rows that see it and no others. An element of the value, or of the key."""
+    Hkv, page, lens = 2, 16, [400, 210]
+    cache, table = filled(lens, Hkv, page, d, E4M3, seed=8)
+    Q = randn(2, Hq, N, d, seed=80)
+    O, lse = P.paged_attention(Q, cache, table, ints(lens), **mask)
+    top = float(np.nanmax(np.abs(values(cache)[1])))
+    G, b = Hq // Hkv, 1
+    left, right, sinks = (lens[b] if v < 0 else v for v in mask.values())
+    p = np.arange(N) + lens[b] - N
+    for at in (lens[b] - 1, lens[b] - 2, lens[b] - N, lens[b] - N - 2, 4):
+        see = torch.from_numpy((at <= p + right) & ((at >= p - left) | (at < sinks))).cuda()
+        i, r = int(table[b, at // page]), at % page
+        for key in (False, True):
+            written, lost = (P.PagedCache(*(t.clone() for t in cache)) for _ in range(2))
+            new = [randn(1, Hkv, 1, d, seed=82 + k) for k in range(2)]
+            new[0 if key else 1][0, 1, 0, 7] = what
+            P.cache_write(*new, written, table[b:b + 1].contiguous(), ints([at + 1]))
+            for t, w in ((lost.K, written.K), (lost.k_scale, written.k_scale)) if key else ((lost.V, written.V), (lost.v_scale, written.v_scale)):
+                assert w[i, 1, r].float().isnan().all()
+                t[i, 1, r] = w[i, 1, r]
+            got, glse = P.paged_attention(Q, lost, table, ints(lens), **mask)
+            assert torch.equal(got[0], O[0]) and torch.equal(got[b, :G], O[b, :G])
+            assert got[b, G:, see].isnan().all()
+            if key:
+                assert glse[b, G:, see].isnan().all() and torch.equal(glse[b, :, ~see], lse[b, :, ~see])
+                assert torch.equal(got[b, :, ~see], O[b, :, ~see])
+            else:
+                assert torch.equal(glse, lse)
+                off = (got[b].float() - O[b].float())[:, ~see].abs()
+                # p rounded once or not at all, either O rounded
+                assert not off.numel() or float(off.max()) <= T.SLACK * 3 * T.U * top
+    P.device_error()
