@@ -29,8 +29,12 @@
 //
 // A value that is no finite number and that only some rows of its tile see would reach the others
 // through a weight of zero. Looking at every such tile for it cost 5% (2 x 24 heads of 4096 x 128,
-// 512 keys to either side: 156 us against 148); the rows' output is looked at instead, and rows that
-// hold something that is no finite number are summed again (mend_rows).
+// 512 keys to either side: 156 us against 148); the rows' output is looked at instead. Items with a
+// row that holds something that is no finite number are marked, and once the CTA is through it takes
+// those again (a second pass of the same roles): such values leave the tiles that some row sees in
+// part, and the rows that see them take them by themselves. No role of the first pass waits for it, and
+// it costs a marked item what the first did, besides the search for the values (an infinity in the last
+// tile of a causal head of 16384 x 128: 672 us, 248 without; of a million tokens: 297 ms, 280 without).
 //
 // Bound: at D = 128 a tile of 128 x 128 takes 2 x 512 cycles of tensor time, and a pair of tiles
 // 2 x 512 x 2 = 2048, as long as its 2 x 16384 exponentials take at 16 per cycle. Measured, a pair
@@ -111,7 +115,11 @@ struct AttendTcCfg {
   // Paged: bit i = page i of the tile is seen and held, for tile t at t % kHeld. Producer, converters
   // and softmax are at most 7 tiles apart.
   static constexpr int OFF_HELD = OFF_MISC + 16, kHeld = 16;
-  static constexpr int SMEM = OFF_HELD + 4 * kHeld + 1024;
+  // The items to take again: bit i of these words for the CTA's items i, i + 32 kMarks, ... (an item
+  // that is taken again without need keeps what it has). Barriers of the second pass.
+  static constexpr int OFF_MARKS = OFF_HELD + 4 * kHeld, kMarks = 32;
+  static constexpr int OFF_BAR2 = OFF_MARKS + 4 * kMarks;
+  static constexpr int SMEM = OFF_BAR2 + 8 * NBARS + 1024;
   static constexpr int S_COL = 0, O_COL = 256;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -281,6 +289,10 @@ struct AttendItem {
   Sight see[2], both;
   TileList tiles;
   bool real;
+  // some row of a group that sees a part of [j0, j0 + 128) does not see all of it
+  __device__ __forceinline__ bool edge(const Window& win, int j0) const {
+    return (see[0].any(j0) && !see[0].all(win, j0, n)) || (see[1].any(j0) && !see[1].all(win, j0, n));
+  }
 };
 // The CTA's items in turn: every gridDim.x-th, its coordinates kept by addition (a runtime division
 // costs a role more than a hundred cycles, and there were six).
@@ -313,6 +325,25 @@ struct ItemWalk {
     if (pair >= p.pairs) pair -= p.pairs, ++split;
     if (split >= p.splits) split -= p.splits, ++hk;
     if (hk >= p.Hkv) hk -= p.Hkv, ++b;
+  }
+};
+// The items of a pass: all of the CTA's, or in the second pass those that are marked.
+template <bool AGAIN>
+struct Items : ItemWalk {
+  const uint32_t* marks;
+  int i = 0;
+  __device__ __forceinline__ Items(const AttendTcParams& p, const uint32_t* m) : ItemWalk(p), marks(m) { skip(p); }
+  __device__ __forceinline__ void skip(const AttendTcParams& p) {
+    if constexpr (AGAIN)
+      while (more(p) && !((marks[(i >> 5) % AttendTcCfg<64, kKvPlain>::kMarks] >> (i & 31)) & 1u)) {
+        ItemWalk::advance(p);
+        ++i;
+      }
+  }
+  __device__ __forceinline__ void advance(const AttendTcParams& p) {
+    ItemWalk::advance(p);
+    ++i;
+    skip(p);
   }
 };
 // The item at `at` (which is one).
@@ -376,154 +407,117 @@ __device__ __forceinline__ void load8(const void* x, const float* scales, int64_
   }
 }
 
-// Rows whose O holds something that is no finite number although their sum is one: a value that the
-// row does not see may have got into it, since the product multiplies it by a weight of zero. If a
-// tile that the rows see a part of holds such a value, those columns are summed again over the visible
-// keys alone. Called by a warp, one row per lane (token < 0: nothing odd in it); out of line, for the others.
+// The cache's row of key j of the item's sequence and key head (the plain one's), -1 if no page holds it.
+template <int KV>
+__device__ __forceinline__ int64_t row_of(const AttendTcParams& p, const AttendItem& w, int j) {
+  if constexpr (KV == kKvPlain) return int64_t(w.bh) * p.N + j;
+  const int page = p.pages.table[size_t(w.b) * p.pages.max_pages + (j >> p.pages.log_page)];
+  if (page < 0 || page >= p.pages.num_pages) return -1;
+  return ((int64_t(page) * p.Hkv + w.hk) << p.pages.log_page) + (j & ((1 << p.pages.log_page) - 1));
+}
+
+// A key (that a row sees) whose value is NaN throughout: the row is NaN by right.
 template <int D, int KV>
-__device__ __noinline__ void mend_rows(const AttendTcParams& p, const ItemWalk item, int g, int token, size_t row, float m,
-                                       float l) {
+__device__ __noinline__ bool lost_value(const AttendTcParams& p, const AttendItem& w, int j) {
+  const int64_t at = row_of<KV>(p, w, j);
+  bool nan = at >= 0;
+#pragma unroll 1
+  for (int c = 0; nan && c < D; c += 8) {
+    float v[8];
+    load8<D, KV>(p.pages.V, p.pages.vs, at, c, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) nan = nan && v[k] != v[k];
+  }
+  return nan;
+}
+
+// Output of the second pass, by a warp, a row per lane: the values that were left out of the tiles that
+// some row sees in part join the rows that see them, and what the first pass left not finite is
+// replaced (`inv` times the sums in tensor memory at `o_addr`; `to`: the row in O, or in the partial
+// sums). A row sees keys up to z, and from a on or below the first tokens' end. Work: a search of
+// the tiles for those seen in part (a lane per tile), and of those few (a lane per key).
+template <int D, int KV>
+__device__ __noinline__ void mend_rows(const AttendTcParams& p, const AttendItem& w, const Sight& mine, bool real, int z,
+                                       int a, size_t to, uint32_t o_addr, float inv) {
   const int lane = threadIdx.x & 31;
-  const AttendItem w = attend_item<KV>(p, item);
-  const Sight mine = g ? w.see[1] : w.see[0];
-  auto row_of = [&](int j) -> int64_t {
-    if constexpr (KV == kKvPlain) return int64_t(w.bh) * p.N + j;
-    const int page = p.pages.table[size_t(w.b) * p.pages.max_pages + (j >> p.pages.log_page)];
-    if (page < 0 || page >= p.pages.num_pages) return -1;
-    return ((int64_t(page) * p.Hkv + w.hk) << p.pages.log_page) + (j & ((1 << p.pages.log_page) - 1));
-  };
-  bool spread = false;
+  auto odd = [](float x) { return !(fabsf(x) < INFINITY); };
 #pragma unroll 1
-  for (int i = w.tiles.from; i < w.tiles.to; ++i) {
-    const int j0 = w.tiles.key(i);
-    if (!mine.any(j0) || mine.all(p.win, j0, w.n)) continue;
-#pragma unroll 1
-    for (int j = j0 + lane; j < min(j0 + 128, w.n); j += 32) {
-      // pages that no row sees are not looked up: their entries may hold anything
-      if (KV != kKvPlain && !(j < w.both.sk || (j >= w.both.lo && j < w.both.hi))) continue;
-      const int64_t at = row_of(j);
-      if (at < 0) continue;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 8) {
-        float v[8];
-        load8<D, KV>(p.pages.V, p.pages.vs, at, c, v);
+  for (int c = 0; c < D; c += 16) {
+    uint32_t o[16];
+    float x[16];
+    __syncwarp();
+    tc::tmem_ld16(o_addr + c, o);
+    tc::tmem_wait_ld(o);
+    bool open = false;  // a column that is NaN takes nothing any more
 #pragma unroll
-        for (int k = 0; k < 8; ++k) spread |= !(fabsf(v[k]) < INFINITY);
+    for (int k = 0; k < 16; ++k) {
+      x[k] = __uint_as_float(o[k]) * inv;
+      open |= x[k] == x[k];
+    }
+    if (__any_sync(0xffffffffu, real && open)) {
+#pragma unroll 1
+      for (int i0 = w.tiles.from; i0 < w.tiles.to; i0 += 32) {
+        const int mine_i = w.tiles.key(i0 + lane);
+        uint32_t tiles = __ballot_sync(0xffffffffu, i0 + lane < w.tiles.to && mine.any(mine_i) && w.edge(p.win, mine_i));
+#pragma unroll 1
+        for (; tiles; tiles &= tiles - 1)
+#pragma unroll 1
+          for (int s = 0; s < 128; s += 32) {
+            const int j0 = w.tiles.key(i0 + __ffs(tiles) - 1) + s;
+            // pages that no row sees are not looked up: their entries may hold anything
+            const int64_t at = mine.any(j0 + lane, 1) ? row_of<KV>(p, w, j0 + lane) : -1;
+            bool bad = false;
+            float v[2][8];
+            if (at >= 0) {
+              load8<D, KV>(p.pages.V, p.pages.vs, at, c, v[0]);
+              load8<D, KV>(p.pages.V, p.pages.vs, at, c + 8, v[1]);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) bad |= odd(v[k >> 3][k & 7]);
+            }
+            uint32_t keys = __ballot_sync(0xffffffffu, bad);
+#pragma unroll 1
+            for (; keys; keys &= keys - 1) {
+              const int j = j0 + __ffs(keys) - 1;
+              const int64_t key = __shfl_sync(0xffffffffu, at, __ffs(keys) - 1);
+              load8<D, KV>(p.pages.V, p.pages.vs, key, c, v[0]);
+              load8<D, KV>(p.pages.V, p.pages.vs, key, c + 8, v[1]);
+              const bool sees = j <= z && (j >= a || j < p.win.sinks);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if (sees && odd(v[k >> 3][k & 7])) x[k] += v[k >> 3][k & 7];
+            }
+          }
       }
     }
-  }
-  if (!__any_sync(0xffffffffu, spread) || token < 0) return;
-  const int pos = w.n - w.nq + (g ? w.t0[1] : w.t0[0]) + token;
-  const int z = min(w.n - 1, pos + p.win.right), a = max(0, pos - p.win.left);
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  const size_t to = size_t(w.split) * size_t(p.B) * p.Hq * p.N + row;
-  // a row that sees a key whose value is NaN throughout keeps its NaN: once a sequence is lost, all do
-#pragma unroll 1
-  for (int i = w.tiles.from; i < w.tiles.to; ++i) {
-    const int j0 = w.tiles.key(i);
-    if (!mine.any(j0) || mine.all(p.win, j0, w.n)) continue;
-#pragma unroll 1
-    for (int j = j0; j < j0 + 128 && j <= z; ++j) {
-      const int64_t at = j >= a || j < p.win.sinks ? row_of(j) : -1;
-      bool nan = at >= 0;
-#pragma unroll 1
-      for (int c = 0; nan && c < D; c += 8) {
-        float v[8];
-        load8<D, KV>(p.pages.V, p.pages.vs, at, c, v);
+    if (!real) continue;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) nan = nan && v[k] != v[k];
+    for (int k = 0; k < 16; ++k) {
+      if (p.splits > 1) {
+        float* f = p.part + to * D + c + k;
+        if (odd(*f)) *f = x[k];
+      } else {
+        bf16* f = p.O + to * D + c + k;
+        if (odd(__bfloat162float(*f))) *f = __float2bfloat16(x[k]);
       }
-      if (nan) return;
-    }
-  }
-  float acc[D];
-#pragma unroll 1
-  for (int c = 0; c < D; ++c) acc[c] = 0.f;
-#pragma unroll 1
-  for (int i = w.tiles.from; i < w.tiles.to; ++i) {
-    const int j0 = w.tiles.key(i);
-#pragma unroll 1
-    for (int j = j0; j < j0 + 128 && j <= z; ++j) {
-      if (j < a && j >= p.win.sinks) continue;
-      const int64_t at = row_of(j);
-      if (at < 0) continue;
-      float s = 0.f, x[8], y[8];
-#pragma unroll 1
-      for (int c = 0; c < D; c += 8) {
-        load8<D, kKvPlain>(p.Q, nullptr, int64_t(row), c, x);
-        load8<D, KV>(p.pages.K, p.pages.ks, at, c, y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s = fmaf(x[k], y[k], s);
-      }
-      const float e = tc::ex2(fmaf(s, p.scale * 1.4426950408889634f, -m));
-#pragma unroll 1
-      for (int c = 0; c < D; c += 8) {
-        load8<D, KV>(p.pages.V, p.pages.vs, at, c, x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[c + k] = fmaf(e, x[k], acc[c + k]);
-      }
-    }
-  }
-#pragma unroll 1
-  for (int c = 0; c < D; ++c) {
-    if (p.splits > 1) {
-      float* x = p.part + to * D + c;
-      if (!(fabsf(*x) < INFINITY)) *x = acc[c] * inv;
-    } else {
-      bf16* x = p.O + row * D + c;
-      if (!(fabsf(__bfloat162float(*x)) < INFINITY)) *x = __float2bfloat16(acc[c] * inv);
     }
   }
 }
 
-template <int D, int KV>
-__global__ void __launch_bounds__(384, 1)
-attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttendTcParams p) {
+// The roles of one pass over the CTA's items (AGAIN: the marked ones, see above). Counters of ring stages
+// and barrier phases start with it: either pass has barriers of its own.
+template <int D, int KV, bool AGAIN>
+__device__ __forceinline__ void attend_pass(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                            const AttendTcParams& p, uint8_t* base, uint32_t base_u, uint32_t tmem) {
   using C = AttendTcCfg<D, KV>;
   using namespace tc;
-  extern __shared__ __align__(16) uint8_t attend_smem[];
-  const uint32_t raw_u = smem_u32(attend_smem);
-  const uint32_t base_u = (raw_u + 1023u) & ~1023u;
-  uint8_t* base = attend_smem + (base_u - raw_u);
+  constexpr bool LANDS = KV == kKvPaged || (KV == kKvPlain && AGAIN);  // warp 2 goes over V's tiles
   volatile int* abort_flag = reinterpret_cast<int*>(base + C::OFF_MISC) + 1;
-  asm volatile("griddepcontrol.launch_dependents;");
   uint32_t* held_mask = reinterpret_cast<uint32_t*>(base + C::OFF_HELD);
-  const uint32_t bar0 = base_u + C::OFF_BAR;
+  uint32_t* marks = reinterpret_cast<uint32_t*>(base + C::OFF_MARKS);
+  const uint32_t bar0 = base_u + (AGAIN ? C::OFF_BAR2 : C::OFF_BAR);
 #define ABAR(i) (bar0 + 8u * uint32_t(i))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::NS; ++s) {
-      mbar_init(ABAR(C::B_FULL + s), C::CODES ? 2 : 1);
-      mbar_init(ABAR(C::B_EMPTY + s), 1);
-    }
-    for (int s = 0; s < C::NL; ++s) {
-      mbar_init(ABAR(C::B_LAND + s), 1);
-      mbar_init(ABAR(C::B_LEMPTY + s), 2);
-    }
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(ABAR(C::B_Q + g), 1);
-      mbar_init(ABAR(C::B_QEMPTY + g), 1);
-      mbar_init(ABAR(C::B_S + g), 1);
-      mbar_init(ABAR(C::B_P + g), 4);
-      mbar_init(ABAR(C::B_H + g), 4);
-      mbar_init(ABAR(C::B_O + g), 1);
-    }
-    mbar_init(ABAR(C::B_END), 1);
-    *abort_flag = 0;
-    mbar_init_fence();
-  }
-  if (warp == 2) {
-    tmem_alloc(base_u + C::OFF_MISC, 512);
-    tmem_relinquish();
-    tc_fence_before();
-  }
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<uint32_t*>(base + C::OFF_MISC);
-
-  // Every role walks the CTA's items; counters of ring stages and barrier phases run on.
   if (warp == 0) {
     // ------------------------------------------------------------- producer
     // Of an item's i-th tile, K is stage use 2 i and V 2 i + 1 behind the items before. Plain keys: lanes
@@ -532,7 +526,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     bool ok = true;
     int use = 0;
     constexpr int NL = C::NL;  // the stages that the copies land in: the ring's, or those for codes
-    for (ItemWalk at(p); at.more(p) && ok; at.advance(p)) {
+    for (Items<AGAIN> at(p, marks); at.more(p) && ok; at.advance(p)) {
       const AttendItem w = attend_item<KV>(p, at);
       if (!w.real) continue;
       const int per = 128 >> p.pages.log_page, size = 1 << p.pages.log_page;
@@ -553,7 +547,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           ok = __all_sync(0xffffffffu, wait_bounded(ABAR((C::CODES ? C::B_LEMPTY : C::B_EMPTY) + s), ((use / NL) & 1) ^ 1, abort_flag));
           if (!ok) break;
           const uint32_t dst = base_u + (C::CODES ? C::OFF_CODES + s * C::LAND : C::OFF_RING + s * C::TILE);
-          const uint32_t bar = ABAR((C::CODES || (KV == kKvPaged && kv) ? C::B_LAND : C::B_FULL) + s);
+          const uint32_t bar = ABAR((C::CODES || (LANDS && kv) ? C::B_LAND : C::B_FULL) + s);
           if constexpr (KV == kKvPlain) {
             if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE);
             __syncwarp();
@@ -575,7 +569,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     // no copy may still be in flight when the CTA exits
     if (lane == 0)
       for (int u = use > NL ? use - NL : 0; u < use; ++u) {
-        if (KV == kKvPaged && (u & 1)) wait_drain(ABAR(C::B_LAND + u % NL), landed_parity<NL>(u));
+        if (LANDS && (u & 1)) wait_drain(ABAR(C::B_LAND + u % NL), landed_parity<NL>(u));
         else wait_drain(ABAR((C::CODES ? C::B_LAND : C::B_FULL) + u % NL), (u / NL) & 1);
       }
   } else if (warp == 1) {
@@ -587,8 +581,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     int use = 0;                // stage uses of the items before
     auto stage = [&](int u) { return base_u + C::OFF_RING + (u % C::NS) * C::TILE; };
     auto full = [&](int u) { return wait_warp(ABAR(C::B_FULL + u % C::NS), (u / C::NS) & 1, abort_flag); };
-    ItemWalk at(p);
-    AttendItem w = attend_item<KV>(p, at), next = w;  // the grid has no more CTAs than there are items
+    Items<AGAIN> at(p, marks);
+    AttendItem w = attend_item<KV>(p, at), next = w;  // the grid has no more CTAs than there are items, and a second pass has one
     while (at.more(p) && ok) {
       const int count = w.tiles.to - w.tiles.from;
       bool looked = false;
@@ -685,7 +679,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     bool ok = true;
     int use = 0;
     uint32_t n_q = 0, q_loaded = 0;  // bit g: phase of the queries, some were loaded
-    for (ItemWalk at(p); at.more(p) && ok; at.advance(p)) {
+    for (Items<AGAIN> at(p, marks); at.more(p) && ok; at.advance(p)) {
       const AttendItem w = attend_item<KV>(p, at);
       if (!w.real) continue;
       const int count = w.tiles.to - w.tiles.from;
@@ -746,16 +740,16 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           warp_arrive(ABAR(C::B_FULL + s));
           warp_arrive(ABAR(C::B_LEMPTY + sl));
         }
-      } else if constexpr (KV == kKvPaged) {
+      } else if constexpr (LANDS) {
         if (warp == 2) {
           for (int u = use + 1; u < use + 2 * count; u += 2) {
             const int s = u % C::NS, j0 = w.tiles.key(w.tiles.from + ((u - use) >> 1));
             ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_LAND + s), landed_parity<C::NS>(u), abort_flag));
             if (!ok) break;
-            const uint32_t held = held_mask[(u >> 1) % C::kHeld];
+            const uint32_t held = KV == kKvPaged ? held_mask[(u >> 1) % C::kHeld] : 0u;
             // values of rows that the window's or the sequence's edge leaves out
             const bool inner = j0 + 128 <= w.both.sk || (j0 >= w.both.lo && j0 + 128 <= w.both.hi);
-            if (!(inner && held == (1u << (128 >> p.pages.log_page)) - 1u)) {
+            if (KV == kKvPaged && !(inner && held == (1u << (128 >> p.pages.log_page)) - 1u)) {
               for (int r = lane; r < 128; r += 32) {
                 const int j = j0 + r;
                 const bool in = ((held >> (r >> p.pages.log_page)) & 1u) && (j < w.both.sk || (j >= w.both.lo && j < w.both.hi));
@@ -765,6 +759,15 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     for (int c = 0; c < 8; ++c)
                       *reinterpret_cast<uint4*>(base + C::OFF_RING + s * C::TILE + pn * 16384 + r * 128 + c * 16) =
                           make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+            }
+            if (AGAIN && w.edge(p.win, j0)) {  // values that are no finite numbers: mend_rows adds them
+#pragma unroll 1
+              for (int x = lane; x < C::TILE / 16; x += 32) {
+                uint4* v = reinterpret_cast<uint4*>(base + C::OFF_RING + s * C::TILE) + x;
+                if (any_not_finite(*v))
+                  *v = make_uint4(finite_or_zero(v->x), finite_or_zero(v->y), finite_or_zero(v->z), finite_or_zero(v->w));
               }
               fence_proxy_async_smem();
             }
@@ -790,7 +793,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     bool ok = true;
     uint32_t n_s = 0, n_o = 0;
     int use = 0;  // stage uses of the items before
-    for (ItemWalk at(p); at.more(p) && ok; at.advance(p)) {
+    for (Items<AGAIN> at(p, marks); at.more(p) && ok; at.advance(p)) {
       const AttendItem w = attend_item<KV>(p, at);
       if (!w.real) continue;
       const Sight mine = g ? w.see[1] : w.see[0];
@@ -817,7 +820,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         float* f = reinterpret_cast<float*>(&next_v);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (!(j + k < mine.sk || (j + k >= mine.lo && j + k < mine.hi))) f[k] = 0.f;
+          if (!(j + k < mine.sk || (j + k >= mine.lo && j + k < mine.hi)) ||
+              (AGAIN && !(fabsf(f[k]) < INFINITY) && w.edge(p.win, w.tiles.key(i))))
+            f[k] = 0.f;
       };
       if constexpr (C::CODES) fetch_scales(w.tiles.from);
       float m = -INFINITY, l = 0.f;
@@ -929,6 +934,12 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const float inv = l != 0.f ? 1.f / l : 0.f;  // l is NaN if a score was
       const bool split_out = p.splits > 1;
       const size_t to = size_t(w.split) * size_t(p.B) * p.Hq * p.N + row;
+      if constexpr (AGAIN) {
+        if (done) mend_rows<D, KV>(p, w, mine, real, z, a, split_out ? to : row, o_addr, inv);
+        tc_fence_before();
+        use += 2 * (w.tiles.to - w.tiles.from);
+        continue;
+      }
       float zero[2] = {0.f, 0.f};  // NaN once a value is no finite number
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
@@ -958,17 +969,92 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         else if (p.lse) p.lse[row] = lg * 0.6931471805599453f;
       }
       const bool odd = real && done && zero[0] + zero[1] != 0.f && l == l;
-      if (__any_sync(0xffffffffu, odd)) mend_rows<D, KV>(p, at, g, odd ? my_token : -1, row, m, l);
+      // a row whose own value is lost is left alone: in a sequence that is lost from a token on, few items are marked
+      if (__any_sync(0xffffffffu, odd && !(pos >= 0 && pos <= z && lost_value<D, KV>(p, w, pos))) && lane == 0) {
+        const uint32_t item = uint32_t(at.id) / gridDim.x;
+        atomicOr(marks + (item >> 5) % C::kMarks, 1u << (item & 31));
+        reinterpret_cast<volatile int*>(base + C::OFF_MISC)[2] = 1;
+      }
       tc_fence_before();
       use += 2 * (w.tiles.to - w.tiles.from);
     }
   }
+#undef ABAR
+}
+
+// The second pass: rare, and out of line so that the first pass keeps its registers.
+template <int D, int KV>
+__device__ __noinline__ void attend_again(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                          const AttendTcParams& p, uint8_t* base, uint32_t base_u, uint32_t tmem) {
+  attend_pass<D, KV, true>(tmQ, tmK, tmV, p, base, base_u, tmem);
+}
+
+template <class C>
+__device__ __forceinline__ void init_barriers(uint32_t bar0) {
+  using tc::mbar_init;
+#define ABAR(i) (bar0 + 8u * uint32_t(i))
+  for (int s = 0; s < C::NS; ++s) {
+    mbar_init(ABAR(C::B_FULL + s), C::CODES ? 2 : 1);
+    mbar_init(ABAR(C::B_EMPTY + s), 1);
+  }
+  for (int s = 0; s < C::NL; ++s) {
+    mbar_init(ABAR(C::B_LAND + s), 1);
+    mbar_init(ABAR(C::B_LEMPTY + s), 2);
+  }
+  for (int g = 0; g < 2; ++g) {
+    mbar_init(ABAR(C::B_Q + g), 1);
+    mbar_init(ABAR(C::B_QEMPTY + g), 1);
+    mbar_init(ABAR(C::B_S + g), 1);
+    mbar_init(ABAR(C::B_P + g), 4);
+    mbar_init(ABAR(C::B_H + g), 4);
+    mbar_init(ABAR(C::B_O + g), 1);
+  }
+  mbar_init(ABAR(C::B_END), 1);
+  tc::mbar_init_fence();
+#undef ABAR
+}
+
+template <int D, int KV>
+__global__ void __launch_bounds__(384, 1)
+attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttendTcParams p) {
+  using C = AttendTcCfg<D, KV>;
+  using namespace tc;
+  extern __shared__ __align__(16) uint8_t attend_smem[];
+  const uint32_t raw_u = smem_u32(attend_smem);
+  const uint32_t base_u = (raw_u + 1023u) & ~1023u;
+  uint8_t* base = attend_smem + (base_u - raw_u);
+  volatile int* misc = reinterpret_cast<int*>(base + C::OFF_MISC);  // tensor memory, abort flag, items to take again
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int warp = threadIdx.x >> 5;
+
+  if (threadIdx.x == 0) {
+    misc[1] = misc[2] = 0;
+    init_barriers<C>(base_u + C::OFF_BAR);
+  }
+  if (warp == 2) {
+    tmem_alloc(base_u + C::OFF_MISC, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  if (warp == 3) reinterpret_cast<uint32_t*>(base + C::OFF_MARKS)[threadIdx.x & 31] = 0;
+  static_assert(C::kMarks == 32, "a lane per word");
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uint32_t(misc[0]);
+  attend_pass<D, KV, false>(tmQ, tmK, tmV, p, base, base_u, tmem);
+  __syncthreads();
+  if (misc[2] && !misc[1]) {
+    tc_fence_after();
+    if (threadIdx.x == 0) init_barriers<C>(base_u + C::OFF_BAR2);
+    __syncthreads();
+    attend_again<D, KV>(tmQ, tmK, tmV, p, base, base_u, tmem);
+    __syncthreads();
+  }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-#undef ABAR
 }
 
 // Joins the runs of a row: weights 2^(lse_s - max), in run order. D / 4 lanes per row, whose loads of

@@ -323,3 +323,25 @@ def test_a_sequence_that_is_lost_from_a_token_on(d):
             assert torch.isfinite(lse[:, :, :at]).all()
             assert bool(torch.isnan(lse[:, :, at:]).all()) == lose_keys
     P.device_error()
+
+
+@pytest.mark.parametrize("what", [float("inf"), float("nan")], ids=["inf", "nan"])
+def test_a_value_that_is_not_finite_at_the_end_of_a_long_sequence(what):
+    """A million keys: the rows beside the value hold what they held however long they are, every other
+    row keeps its bits, and nothing runs out of time."""
+    N, d, at, c = 2 ** 20 + 37, 64, 2 ** 20 + 30, 5
+    g = torch.Generator(device="cuda").manual_seed(53)
+    Q, K, V = (torch.randn(1, h, N, d, device="cuda", generator=g).to(torch.bfloat16) for h in (2, 1, 1))
+    O, lse = P.window_attention(Q, K, V, right=0)
+    bad = V.clone()
+    bad[0, 0, at, c] = what
+    got, glse = P.window_attention(Q, K, bad, right=0)
+    P.device_error()
+    assert torch.equal(glse, lse) and torch.isfinite(O.float()).all()
+    col = got[:, :, :, c].clone()
+    assert (col[:, :, at:].isnan() if what != what else col[:, :, at:] == what).all()
+    # p rounded in either sum, and either O
+    off = (col.float() - O[:, :, :, c].float())[:, :, :at].abs()
+    assert float(off.max()) <= T.SLACK * 4 * T.U * float(V[0, 0, :, c].abs().max())
+    got[:, :, :, c] = O[:, :, :, c]
+    assert torch.equal(got, O)
