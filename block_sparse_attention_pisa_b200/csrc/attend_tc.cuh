@@ -82,6 +82,7 @@ struct AttendTcParams {
   int part_pairs;   // of one part of its heads
   int splits;       // runs that a piece's tile list is cut into
   int items;        // pairs * B * Hkv * splits
+  long long patience;  // cycles that all of a CTA's items may take
   Window win;
   float scale;
 };
@@ -206,6 +207,25 @@ __device__ __forceinline__ bool elect() {
 // wait of a whole warp that issues products
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, tc::wait_poll(bar, parity, abort_flag));
+}
+
+// Wait of a warp for what may lie an item or more ahead (scores of a group that has no rows in the items
+// before, the last scores over the item before): bounded by what all items may take, where other waits
+// are bounded by about a second.
+__device__ __forceinline__ bool wait_item(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long patience) {
+  bool ok = tc::mbar_try_wait(bar, parity);
+  if (!ok) {
+    const long long t0 = clock64();
+    while (!(ok = tc::mbar_try_wait(bar, parity))) {
+      if (*abort_flag) break;
+      if (clock64() - t0 > tc::kWaitCycles + patience) {
+        *abort_flag = 1;
+        flag_error(kErrTimeout);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 
 // 4 x 4 transposition of 16-byte pieces among the lanes of a quad
@@ -688,7 +708,7 @@ __device__ __forceinline__ void attend_pass(const CUtensorMap& tmQ, const CUtens
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           if (w.see[g].hi == 0) continue;
-          if (ok) ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_QEMPTY + g), ((n_q >> g) & 1u) ^ 1u, abort_flag));
+          if (ok) ok = wait_item(ABAR(C::B_QEMPTY + g), ((n_q >> g) & 1u) ^ 1u, abort_flag, p.patience);
           if (ok && lane == 0) {
             mbar_arrive_expect_tx(ABAR(C::B_Q + g), p.rt.tokens * p.rt.heads * D * 2);
 #pragma unroll
@@ -839,7 +859,7 @@ __device__ __forceinline__ void attend_pass(const CUtensorMap& tmQ, const CUtens
           fetch_scales(i + 1);
           __syncwarp();
         }
-        ok = __all_sync(0xffffffffu, wait_bounded(ABAR(C::B_S + g), n_s, abort_flag));
+        ok = wait_item(ABAR(C::B_S + g), n_s, abort_flag, p.patience);
         if (!ok) break;
         n_s ^= 1u;
         tc_fence_after();

@@ -177,6 +177,10 @@ template <int D, int KV>
 pisa_status_t launch_attend_tc(pisa::AttendTcParams p, const void* K, const void* V, int page, int num_pages,
                                void* workspace, cudaStream_t st) {
   using C = pisa::AttendTcCfg<D, KV>;
+  const int ctas = p.items < kSms ? p.items : kSms;
+  // twice the cycles that a pair of tiles takes, for every tile of the CTA's items
+  const int64_t cap = KV == pisa::kKvPlain ? p.N : int64_t(p.pages.max_pages) * page;
+  p.patience = int64_t((p.items + ctas - 1) / ctas) * (cap / 128 / p.splits + 2) * 8192;
   CUtensorMap mQ, mK, mV;
   PISA_TRY(make_rows_map(&mQ, p.Q, D, uint64_t(p.N), uint64_t(p.B) * p.Hq, uint32_t(p.rt.tokens), uint32_t(p.rt.heads)));
   if constexpr (KV == pisa::kKvPlain) {
@@ -198,7 +202,7 @@ pisa_status_t launch_attend_tc(pisa::AttendTcParams p, const void* K, const void
   }
   auto k = pisa::attend_tc_kernel<D, KV>;
   PISA_TRY(set_smem(k, C::SMEM));
-  k<<<unsigned(p.items < kSms ? p.items : kSms), C::kThreads, C::SMEM, st>>>(mQ, mK, mV, p);
+  k<<<unsigned(ctas), C::kThreads, C::SMEM, st>>>(mQ, mK, mV, p);
   PISA_TRY(check_launch("attend_tc_kernel"));
   if (p.splits > 1) {
     constexpr int per = pisa::kJoinThreads / (D / 4);  // rows of a block

@@ -282,7 +282,8 @@ pisa_status_t pisa_run_host_static(const void* Q, const void* K, const void* V, 
  * a row does not see does not reach its O and lse, a NaN or an infinity either. The gradient
  * asks for finite operands: one that is not may reach every gradient of its key head. Every
  * sum runs in an order fixed by the shapes (and, over a cache, by the lengths): the same
- * call gives the same bits.
+ * call gives the same bits. A sum of n keys is off by up to n 2^-24 of sum p|v|, as fp32 sums
+ * are: with like weights and values of one sign by 0.4% at a million keys, 0.9% at two.
  * The conventions above hold (bf16, device pointers of the current device, contiguous,
  * asynchronous, d in {64, 128}); pointers to int32 and to lse need 4-byte alignment only.
  * No output may overlap an input.

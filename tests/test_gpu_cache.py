@@ -575,3 +575,23 @@ def test_a_lost_token_as_the_cache_holds_it(what, N, Hq, d, mask):
                 # p rounded once or not at all, either O rounded
                 assert not off.numel() or float(off.max()) <= T.SLACK * 3 * T.U * top
     P.device_error()
+
+
+def test_a_hundred_million_keys():
+    """Sequences whose walk over the keys takes seconds: a role that waits for the next one's scores or
+    queries does not give up. Keys of zero: lse = log of the keys seen. The sequences share their pages;
+    only one of either tile has rows."""
+    B, N, d, page, n = 300, 17, 64, 128, 110_000_000
+    num = -(-n // page)
+    cache = P.PagedCache(torch.zeros(num, 1, page, d, dtype=BF16, device="cuda"), torch.ones(num, 1, page, d, dtype=BF16, device="cuda"))
+    table = torch.arange(num, dtype=torch.int32, device="cuda").repeat(B, 1)
+    lens = torch.arange(n - B, n, dtype=torch.int32, device="cuda")
+    Q = randn(B, 1, N, d, seed=61)
+    O, lse = torch.full_like(Q, 5.0), torch.full((B, 1, N), 5.0, device="cuda")
+    P.paged_attention(Q, cache, table, lens, out=O, lse=lse)
+    P.device_error()
+    seen = (lens[:, None].double() - N + 1 + torch.arange(N, device="cuda"))[:, None]
+    assert float((lse.double() - seen.log()).abs().max()) <= 2.0 ** -19 + 2.0 ** -22 * 19
+    # a sum of n terms in fp32 is off by up to n 2^-24 of sum p|v| = 1, here 6.6: that the rows were
+    # written is all that can be said of O (the tensor core drops a product below 2^-26 of its sum)
+    assert torch.isfinite(O.float()).all() and not (O == 5).any()
