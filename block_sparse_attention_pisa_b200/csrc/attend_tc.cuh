@@ -35,6 +35,9 @@
 // part, and the rows that see them take them by themselves. No role of the first pass waits for it, and
 // it costs a marked item what the first did, besides the search for the values (an infinity in the last
 // tile of a causal head of 16384 x 128: 672 us, 248 without; of a million tokens: 297 ms, 280 without).
+// It also holds its weights in a frame so far down that sums of the largest values stay in range: a
+// weight may be 2^8 and there are many, so that the first pass leaves the range from values of about
+// 2^120 on (and less, with many keys). What the first pass found finite stays, in full precision.
 //
 // Bound: at D = 128 a tile of 128 x 128 takes 2 x 512 cycles of tensor time, and a pair of tiles
 // 2 x 512 x 2 = 2048, as long as its 2 x 16384 exponentials take at 16 per cycle. Measured, a pair
@@ -845,6 +848,9 @@ __device__ __forceinline__ void attend_pass(const CUtensorMap& tmQ, const CUtens
             f[k] = 0.f;
       };
       if constexpr (C::CODES) fetch_scales(w.tiles.from);
+      // second pass: 2^-c times a weight, so that the run's weights (2^8 at most) sum to no more than one
+      const int c = AGAIN ? 40 - __clz(max(1, w.tiles.to - w.tiles.from) * 128 - 1) : 0;
+      const float frame = exponent(127 - c);
       float m = -INFINITY, l = 0.f;
       uint32_t done = 0;
       for (int i = w.tiles.from; i < w.tiles.to; ++i) {
@@ -925,11 +931,11 @@ __device__ __forceinline__ void attend_pass(const CUtensorMap& tmQ, const CUtens
             sum[k & 3] += e0 + e1;
             if constexpr (C::CODES) {  // the value's scale may be NaN, or the weight huge beside it
               if (k % 2 == 0) f = reinterpret_cast<const float4*>(scales + 128)[ch * 8 + k / 2];
-              uint32_t x0 = __float_as_uint(e0), x1 = __float_as_uint(e1);
+              uint32_t x0 = __float_as_uint(AGAIN ? e0 * frame : e0), x1 = __float_as_uint(AGAIN ? e1 * frame : e1);
               mul2(x0, x1, k % 2 ? f.z : f.x, k % 2 ? f.w : f.y);
               pk[k] = pack_bf16x2(__uint_as_float(x0), __uint_as_float(x1));
             } else {
-              pk[k] = pack_bf16x2(e0, e1);
+              pk[k] = AGAIN ? pack_bf16x2(e0 * frame, e1 * frame) : pack_bf16x2(e0, e1);
             }
           }
           tmem_st16(s_addr + ch * 16, pk);
@@ -955,7 +961,7 @@ __device__ __forceinline__ void attend_pass(const CUtensorMap& tmQ, const CUtens
       const bool split_out = p.splits > 1;
       const size_t to = size_t(w.split) * size_t(p.B) * p.Hq * p.N + row;
       if constexpr (AGAIN) {
-        if (done) mend_rows<D, KV>(p, w, mine, real, z, a, split_out ? to : row, o_addr, inv);
+        if (done) mend_rows<D, KV>(p, w, mine, real, z, a, split_out ? to : row, o_addr, inv * exponent(127 + c));
         tc_fence_before();
         use += 2 * (w.tiles.to - w.tiles.from);
         continue;
@@ -1078,7 +1084,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 }
 
 // Joins the runs of a row: weights 2^(lse_s - max), in run order. D / 4 lanes per row, whose loads of
-// several runs are in flight at once. Bound by memory (the partial sums are read once).
+// several runs are in flight at once. Bound by memory (the partial sums are read once). The sum of the
+// runs (no more than 148) is held 2^8 below its size, in range for any results of theirs.
 constexpr int kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendTcParams p, int paged) {
@@ -1100,14 +1107,14 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendT
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = 0; s < p.splits; ++s) {  // a run that saw nothing holds zeros
-    const float w = tc::ex2(__ldg(p.part_lse + s * rows + row) - m0);
+    const float w = tc::ex2(__ldg(p.part_lse + s * rows + row) - m0) * exponent(127 - 8);
     const float4 x = __ldcs(reinterpret_cast<const float4*>(p.part + (s * rows + row) * D + c));
     l += w;
     o = make_float4(fmaf(w, x.x, o.x), fmaf(w, x.y, o.y), fmaf(w, x.z, o.z), fmaf(w, x.w, o.w));
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
   *reinterpret_cast<uint2*>(p.O + row * D + c) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (c == 0 && p.lse) p.lse[row] = l != 0.f ? (m0 + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (c == 0 && p.lse) p.lse[row] = l != 0.f ? (m0 + __log2f(l * exponent(127 + 8))) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace pisa

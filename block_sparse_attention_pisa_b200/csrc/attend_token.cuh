@@ -29,7 +29,9 @@
 // bf16's 8 bits. The weights (softmax weight times the value's scale) have a factor of their own
 // per row that keeps the largest at 2^6 or more and below 2^15, apart from the maximum that the
 // row's sum is relative to: scales of any size keep 11 bits of every weight down to 2^-20 of the
-// largest. O is in that frame.
+// largest. O is in that frame. In bf16 the weights (2^8 at most) are held 2^-c down, a warp's sum at
+// one or less, and O stays in range for values of any size (values below 2^(c - 126) lose bits: 2^-100).
+// Warps' and CTAs' sums are joined as averages, for the same reason.
 //
 // The visible keys of all sequences and key heads form one list of chunks, cut evenly over
 // the CTAs: sequences of different lengths balance, one long sequence fills the GPU. A CTA
@@ -141,7 +143,7 @@ __device__ __forceinline__ uint4 ldg16(const void* p, bool in) {
   return r;
 }
 
-// Joins the four warps' sums of chunks [c0, c1) of (b, hk), in warp order: rows of O if the CTA
+// Joins the four warps' averages over chunks [c0, c1) of (b, hk), in warp order: rows of O if the CTA
 // holds the whole list, a piece in the workspace if not.
 template <int D, int NR>
 __device__ __forceinline__ void join_warps(const AttendTokenParams& p, const TokenSight& s, int b, int hk, int c0, int c1,
@@ -156,21 +158,24 @@ __device__ __forceinline__ void join_warps(const AttendTokenParams& p, const Tok
 #pragma unroll
     for (int w = 0; w < kTokenWarps; ++w) mm = fmaxf(mm, stat[0][w][r]);
     const float m0 = mm == -INFINITY ? 0.f : mm;
-    float ll = 0.f;
+    float ll = 0.f, part[kTokenWarps];
+#pragma unroll
+    for (int w = 0; w < kTokenWarps; ++w) {
+      part[w] = tc::ex2(stat[0][w][r] - m0) * stat[1][w][r];  // a warp that saw nothing: 0, and its average is 0
+      ll += part[w];
+    }
+    const float inv = ll != 0.f ? 1.f / ll : 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kTokenWarps; ++w) {
-      const float k = tc::ex2(stat[0][w][r] - m0);  // a warp that saw nothing: 0, and its sums are 0
       const float4 y = *reinterpret_cast<const float4*>(&acc[w][r][d]);
-      ll = fmaf(k, stat[1][w][r], ll);
+      const float k = part[w] * inv;
       x.x = fmaf(k, y.x, x.x);
       x.y = fmaf(k, y.y, x.y);
       x.z = fmaf(k, y.z, x.z);
       x.w = fmaf(k, y.w, x.w);
     }
-    const float inv = ll != 0.f ? 1.f / ll : 0.f;
     const float lg = ll != 0.f ? m0 + __log2f(ll) : -INFINITY;
-    x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     if (all) {
       const size_t row = (size_t(b) * p.Hq + hk * G + r % G) * p.N + r / G;
       *reinterpret_cast<uint2*>(p.O + row * D + d) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
@@ -282,6 +287,8 @@ attend_token_kernel(const AttendTokenParams p) {
         if constexpr (E4M3) sl2[h][e] *= __shfl_sync(0xffffffffu, up[h], (2 * q + e) * 4);
       }
     constexpr int kTopField = 247;  // the weights' factor f is at most 2^120
+    const int down = 40 - __clz(max(c1 - c0, 1) * KEYS - 1);  // bf16: c, the weights of a warp's keys sum to 2^c at most
+    const float frame = exponent(127 - down);
     float o[NR][MT][4], m[NR][2], l[NR][2], f[NR][2];
 #pragma unroll
     for (int h = 0; h < NR; ++h) {
@@ -553,7 +560,7 @@ attend_token_kernel(const AttendTokenParams p) {
             for (int t = 0; t < 2; ++t) {
               const float w = tc::ex2(fmaf(sc[i][h][e + 2 * t], sl2[h][e], neg));
               l[h][e] += w;
-              sc[i][h][e + 2 * t] = E4M3 ? w * vs[i][t] : w;
+              sc[i][h][e + 2 * t] = w * (E4M3 ? vs[i][t] : frame);
               if constexpr (E4M3) tm[h][e] = fmaxf(tm[h][e], sc[i][h][e + 2 * t]);
             }
           if constexpr (E4M3) wide |= f[h][e] > exponent(kTopField) || tm[h][e] * f[h][e] > 32768.f;
@@ -619,14 +626,15 @@ attend_token_kernel(const AttendTokenParams p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * h + 2 * q + e;
-        const float k = E4M3 ? 1.f / f[h][e] : 1.f;
+        const float k = E4M3 ? 1.f / f[h][e] : exponent(127 + down);
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], off);
+        const float inv = l[h][e] != 0.f ? 1.f / l[h][e] : 0.f;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           // rows g and 8 + g of product i are neighbouring dimensions
           const int d = E4M3 ? g * (D / 8) + 2 * i : (i >> 2) * 64 + g * 8 + 2 * (i & 3);
-          *reinterpret_cast<float2*>(&acc[warp][r][d]) = make_float2(o[h][i][e] * k, o[h][i][e + 2] * k);
+          *reinterpret_cast<float2*>(&acc[warp][r][d]) = make_float2(o[h][i][e] * inv * k, o[h][i][e + 2] * inv * k);
         }
         if (g == 0) {
           stat[0][warp][r] = m[h][e];
@@ -676,7 +684,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps) attend_token_join_kernel(con
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int c = first + group; c <= last; c += GROUPS) {
-    const float w = tc::ex2(p.part_lse[slot(c)] - m0);
+    const float w = tc::ex2(p.part_lse[slot(c)] - m0) * exponent(127 - 10);  // no more than 592 pieces: in range
     const float4 y = *reinterpret_cast<const float4*>(p.part + slot(c) * D + col * 4);
     l += w;
     x.x = fmaf(w, y.x, x.x);
@@ -697,7 +705,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps) attend_token_join_kernel(con
   const float inv = l != 0.f ? 1.f / l : 0.f;
   const size_t row = (size_t(b) * p.Hq + hk * G + r % G) * p.N + r / G;
   *reinterpret_cast<uint2*>(p.O + row * D + col * 4) = make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-  if (col == 0 && p.lse) p.lse[row] = l != 0.f ? (m0 + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (col == 0 && p.lse) p.lse[row] = l != 0.f ? (m0 + __log2f(l * exponent(127 + 10))) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace pisa

@@ -595,3 +595,23 @@ def test_a_hundred_million_keys():
     # a sum of n terms in fp32 is off by up to n 2^-24 of sum p|v| = 1, here 6.6: that the rows were
     # written is all that can be said of O (the tensor core drops a product below 2^-26 of its sum)
     assert torch.isfinite(O.float()).all() and not (O == 5).any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("N,lens,left", [(1, [5000, 70], -1), (4, [3000, 900], 2000), (70, [1500, 300], -1), (20, [9000], -1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_near_the_end_of_the_range(dtype, N, lens, left, d):
+    """Values of one sign up to 2^126.3 (bf16: beside columns of 2^-90): the sums of exp(s - m) v leave
+    fp32, the averages do not. Single tokens, chunks, sequences cut into runs."""
+    Hkv, page = 2, 32
+    table, total = table_of(lens, page, seed=62)
+    cache = P.paged_cache(total, Hkv, page, d, dtype)
+    K, V = (randn(len(lens), Hkv, max(lens), d, seed=62 + i) for i in range(2))
+    V = (V.float().abs().clamp_max(4) + 0.5) * 2.0 ** 124
+    if dtype == BF16:
+        V[..., ::3] *= 2.0 ** -214
+    P.cache_write(K, V.to(BF16), cache, table, ints(lens), ints(lens))
+    Q = randn(len(lens), 4, N, d, seed=64)
+    O, lse = P.paged_attention(Q, cache, table, ints(lens), left=left)
+    P.device_error()
+    check_attention(O, lse, Q, cache, table, lens, [N] * len(lens), left, 0, 0, d ** -0.5)

@@ -345,3 +345,25 @@ def test_a_value_that_is_not_finite_at_the_end_of_a_long_sequence(what):
     assert float(off.max()) <= T.SLACK * 4 * T.U * float(V[0, 0, :, c].abs().max())
     got[:, :, :, c] = O[:, :, :, c]
     assert torch.equal(got, O)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_near_the_end_of_the_range(d):
+    """Values of one sign up to 2^126.3, beside columns of 2^-90: sums of exp(s - m) v leave fp32, the
+    averages do not. An infinity in between reaches the rows that see it, and no others."""
+    N = 1500
+    Q, K, V, _ = make(1, 4, 2, N, d, seed=54)
+    V = (V.float().abs().clamp_max(4) + 0.5) * 2.0 ** 124
+    V[..., ::3] *= 2.0 ** -214
+    V = V.to(torch.bfloat16)
+    for left, right in ((-1, -1), (700, 0)):
+        O, lse = P.window_attention(Q, K, V, left=left, right=right)
+        check_forward(O, lse, Q, K, V, left, right, 0, d ** -0.5)
+        bad = V.clone()
+        bad[0, 1, 1000, 1] = float("inf")
+        got, glse = P.window_attention(Q, K, bad, left=left, right=right)
+        see = torch.from_numpy(W.visible(np.arange(N), N, left, right, 0)[:, 1000]).cuda()
+        assert torch.equal(glse, lse) and (got[0, 2:, see, 1] == float("inf")).all()
+        got[0, 2:, see, 1] = O[0, 2:, see, 1]
+        check_forward(got, glse, Q, K, V, left, right, 0, d ** -0.5)
+    P.device_error()
