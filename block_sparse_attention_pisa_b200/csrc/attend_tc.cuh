@@ -1087,6 +1087,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 // several runs are in flight at once. Bound by memory (the partial sums are read once). The sum of the
 // runs (no more than 148) is held 2^8 below its size, in range for any results of theirs.
 constexpr int kJoinThreads = 256;
+// Its blocks may start while the partial sums are still written: no loads through the read-only path.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendTcParams p, int paged) {
   constexpr int LANES = D / 4, ROWS = kJoinThreads / LANES;
@@ -1101,13 +1102,13 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendT
   }
   float m = -INFINITY;
 #pragma unroll 4
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, __ldg(p.part_lse + s * rows + row));
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, __ldcg(p.part_lse + s * rows + row));
   const float m0 = m == -INFINITY ? 0.f : m;
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = 0; s < p.splits; ++s) {  // a run that saw nothing holds zeros
-    const float w = tc::ex2(__ldg(p.part_lse + s * rows + row) - m0) * exponent(127 - 8);
+    const float w = tc::ex2(__ldcg(p.part_lse + s * rows + row) - m0) * exponent(127 - 8);
     const float4 x = __ldcs(reinterpret_cast<const float4*>(p.part + (s * rows + row) * D + c));
     l += w;
     o = make_float4(fmaf(w, x.x, o.x), fmaf(w, x.y, o.y), fmaf(w, x.z, o.z), fmaf(w, x.w, o.w));

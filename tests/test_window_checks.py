@@ -1,6 +1,8 @@
 """Refusals of the windowed attention, the paged cache and the attention over it: by the C ABI
 (fake pointers, never dereferenced: the checks come first) and by the binding. CPU only."""
 import ctypes
+import os
+import re
 
 import pytest
 
@@ -193,3 +195,20 @@ def test_binding_refuses_wrong_workspaces():
             P._workspace(bad, 16, cpu)
     assert P._workspace(torch.zeros(16, dtype=torch.uint8), 16, cpu)[1] == 16
     assert P._workspace(None, 0, cpu) == (None, 0, None)
+
+
+# ------------------------------------------------------------------ the sources
+
+def test_kernels_that_start_early_read_no_results_as_constants():
+    """A kernel that starts beside the one before it (and waits) may not load through the read-only
+    path: what it reads may still have been written when it started."""
+    early = 0
+    for name in sorted(os.listdir(B.CSRC)):
+        with open(os.path.join(B.CSRC, name)) as f:
+            text = f.read()
+        for part in re.split(r"(?=__global__ )", text)[1:]:
+            body = part[:part.index("\n}\n")]
+            if "griddepcontrol.wait" in body:
+                early += 1
+                assert not re.search(r"__ldg\b|ldg_stream|ldg16|ld\.global\.nc|__restrict__", body), (name, body[:80])
+    assert early == 4
