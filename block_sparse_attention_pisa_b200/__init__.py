@@ -518,15 +518,51 @@ def _workspace(t, nbytes: int, dev):
     return t.data_ptr(), t.numel(), t
 
 
+_window_function = None
+
+
+def _recorded_window_attention():
+    """``window_attention`` as a torch.autograd.Function (made on first use: torch is imported late here)."""
+    global _window_function
+    if _window_function is None:
+        import torch
+
+        class WindowAttention(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, Q, K, V, left, right, sinks, scale):
+                O, lse = window_attention(Q, K, V, left, right, sinks, scale)
+                ctx.save_for_backward(Q, K, V, O, lse)
+                ctx.mark_non_differentiable(lse)
+                ctx.call = (left, right, sinks, scale)
+                return O, lse
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dO, _):
+                grads = window_attention_backward(dO.contiguous(), *ctx.saved_tensors, *ctx.call)
+                return *(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None, None
+
+        _window_function = WindowAttention
+    return _window_function
+
+
 def window_attention(Q, K, V, left: int = -1, right: int = -1, sinks: int = 0, scale: float | None = None, out=None,
                      lse=None):
     """Self-attention in which the query at position p sees key j if ``j <= p + right`` and
     (``j >= p - left`` or ``j < sinks``); -1 sets no limit on a side. Q: bf16 [B, Hq, N, d];
     K, V: bf16 [B, Hkv, N, d], query head h reading key head ``h // (Hq // Hkv)``. Returns
-    (O bf16 [B, Hq, N, d], lse fp32 [B, Hq, N], the natural logarithm of each row's sum)."""
+    (O bf16 [B, Hq, N, d], lse fp32 [B, Hq, N], the natural logarithm of each row's sum). Autograd
+    records the call: O carries its gradient (``window_attention_backward``'s), lse none, and
+    ``out`` and ``lse`` cannot be given then. PyTorch captures a recorded backward pass only while
+    no eager graph of the same leaves lives; a captured training step calls
+    ``window_attention_backward`` itself."""
     import torch
     B, Hq, N, d = q = _heads(Q, "Q")
     kv, stat = (B, _heads(K, "K")[1], N, d), (B, Hq, N)
+    if torch.is_grad_enabled() and (Q.requires_grad or K.requires_grad or getattr(V, "requires_grad", False)):
+        if out is not None or lse is not None:
+            raise ValueError("out and lse cannot be given while autograd records the call (an operand requires a gradient)")
+        return _recorded_window_attention().apply(Q, K, V, left, right, sinks, scale)
     checks = [(Q, "Q", q, torch.bfloat16), (K, "K", kv, torch.bfloat16), (V, "V", kv, torch.bfloat16)]
     if out is not None:
         checks.append((out, "O", q, torch.bfloat16))

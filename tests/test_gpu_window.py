@@ -367,3 +367,39 @@ def test_values_near_the_end_of_the_range(d):
         got[0, 2:, see, 1] = O[0, 2:, see, 1]
         check_forward(got, glse, Q, K, V, left, right, 0, d ** -0.5)
     P.device_error()
+
+
+def test_autograd_records_the_call():
+    """O carries the gradient that window_attention_backward gives, bit for bit, for the operands that
+    ask for one; nothing is recorded without a need, and a second derivative is refused."""
+    mask = dict(left=70, right=3, sinks=9)
+    Q, K, V, dO = make(1, 4, 2, 333, 64, seed=55)
+    O, lse = P.window_attention(Q, K, V, **mask)
+    assert not O.requires_grad
+    want = P.window_attention_backward(dO, Q, K, V, O, lse, **mask)
+    for need in ((1, 1, 1), (0, 0, 1), (1, 0, 0)):
+        leaves = [torch.nn.Parameter(t.clone(), requires_grad=bool(n)) for t, n in zip((Q, K, V), need)]
+        got, glse = P.window_attention(*leaves, **mask)
+        assert got.requires_grad and not glse.requires_grad
+        assert torch.equal(got, O) and torch.equal(glse, lse)
+        got.backward(dO)
+        for leaf, w, n in zip(leaves, want, need):
+            assert torch.equal(leaf.grad, w) if n else leaf.grad is None
+        with torch.no_grad():
+            assert not P.window_attention(*leaves, **mask)[0].requires_grad
+    # through other operations, scale given, on another stream, and a gradient that is a broadcast scalar
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        leaves = [t.clone().requires_grad_() for t in (Q, K, V)]
+        got, _ = P.window_attention(leaves[0] * 1, leaves[1] * 1, leaves[2] * 1, scale=0.2, **mask)
+        got.sum().backward()
+    torch.cuda.current_stream().wait_stream(s)
+    O, lse = P.window_attention(Q, K, V, scale=0.2, **mask)
+    want = P.window_attention_backward(torch.ones_like(O), Q, K, V, O, lse, scale=0.2, **mask)
+    assert all(torch.equal(x.grad, w) for x, w in zip(leaves, want))
+    got, _ = P.window_attention(*leaves, **mask)
+    (g,) = torch.autograd.grad(got, leaves[0], dO, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+    P.device_error()

@@ -197,6 +197,19 @@ def test_binding_refuses_wrong_workspaces():
     assert P._workspace(None, 0, cpu) == (None, 0, None)
 
 
+def test_outputs_cannot_be_given_while_autograd_records(L):
+    for kw in (dict(out=q()), dict(lse=torch.zeros(1, 4, 8))):
+        for need in range(3):
+            ops = [q(), q(2), q(2)]
+            ops[need].requires_grad_()
+            with pytest.raises(ValueError, match="autograd"):
+                P.window_attention(*ops, **kw)
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # host tensors: refused last
+                P.window_attention(*ops, **kw)
+            with pytest.raises(ValueError, match="CUDA"):
+                P.window_attention(*ops)
+
+
 # ------------------------------------------------------------------ the sources
 
 def test_kernels_that_start_early_read_no_results_as_constants():
