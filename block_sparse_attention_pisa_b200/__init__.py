@@ -607,6 +607,8 @@ def window_attention_backward(dO, Q, K, V, O, lse, left: int = -1, right: int = 
     _launch(lib().pisa_window_attention_backward, dev, dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
             lse.data_ptr(), WindowShape(B, Hq, Hkv, N, d), _window(left, right, sinks), d ** -0.5 if scale is None else float(scale),
             dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws, nbytes)
+    if Hq == 0:  # keys that no query head reads
+        dK.zero_(), dV.zero_()
     return dQ, dK, dV
 
 

@@ -322,8 +322,8 @@ pisa_status_t pisa_window_attention_backward_workspace(pisa_window_shape_t shape
  *   dQ = scale sum_j ds_j k_j,  dK_j = scale sum ds_j q,  dV_j = sum p_j dO
  * (the sums of dK, dV over the rows that see j, of every query head of its group).
  * O and lse as the forward call gave them; dO, dQ: bf16 [B, Hq, N, d]; dK, dV: bf16
- * [B, Hkv, N, d], overwritten. workspace: device memory, 256-byte aligned, scratch; one
- * call at a time may use it.
+ * [B, Hkv, N, d], overwritten (with Hq = 0, as with any size of 0, nothing is touched).
+ * workspace: device memory, 256-byte aligned, scratch; one call at a time may use it.
  */
 pisa_status_t pisa_window_attention_backward(const void* dO, const void* Q, const void* K, const void* V,
                                              const void* O, const float* lse, pisa_window_shape_t shape,

@@ -398,8 +398,18 @@ def test_autograd_records_the_call():
     O, lse = P.window_attention(Q, K, V, scale=0.2, **mask)
     want = P.window_attention_backward(torch.ones_like(O), Q, K, V, O, lse, scale=0.2, **mask)
     assert all(torch.equal(x.grad, w) for x, w in zip(leaves, want))
+    leaves = [t.clone().requires_grad_() for t in (Q, K, V)]
     got, _ = P.window_attention(*leaves, **mask)
     (g,) = torch.autograd.grad(got, leaves[0], dO, create_graph=True)
     with pytest.raises(RuntimeError):
         g.sum().backward()
     P.device_error()
+
+
+def test_keys_without_query_heads_have_no_gradient():
+    """No query head at all: the gradients of the keys and values are zero, preallocated or not."""
+    Q, K = torch.empty(2, 0, 9, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(2, 3, 9, 64, dtype=torch.bfloat16, device="cuda")
+    O, lse = P.window_attention(Q, K, K)
+    out = torch.empty_like(Q), torch.full_like(K, 3.0), torch.full_like(K, 3.0)
+    for grads in (P.window_attention_backward(Q, Q, K, K, O, lse), P.window_attention_backward(Q, Q, K, K, O, lse, out=out)):
+        assert grads[0].shape == Q.shape and all(g.shape == K.shape and (g == 0).all() for g in grads[1:])
