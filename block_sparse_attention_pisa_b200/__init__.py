@@ -579,6 +579,9 @@ def window_attention(Q, K, V, left: int = -1, right: int = -1, sinks: int = 0, s
 def window_attention_backward_workspace(B: int, Hq: int, Hkv: int, N: int, d: int, left: int = -1, right: int = -1,
                                         sinks: int = 0) -> int:
     """Device workspace (bytes) that ``window_attention_backward`` needs for this problem."""
+    for x, name in ((B, "B"), (Hq, "Hq"), (Hkv, "Hkv"), (N, "N"), (d, "d")):
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{name}={x} does not fit 32 bits")
     n = ctypes.c_size_t(0)
     _check(lib().pisa_window_attention_backward_workspace(WindowShape(B, Hq, Hkv, N, d), _window(left, right, sinks),
                                                           ctypes.byref(n)))

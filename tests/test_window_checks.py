@@ -210,6 +210,16 @@ def test_outputs_cannot_be_given_while_autograd_records(L):
                 P.window_attention(*ops)
 
 
+def test_sizes_past_32_bits_are_refused(L):
+    """ctypes would take them modulo 2^32."""
+    good = dict(B=1, Hq=4, Hkv=2, N=8, d=64)
+    assert P.window_attention_backward_workspace(**good) > 0
+    for name in good:
+        for x in (good[name] + 2 ** 32, -2 ** 31 - 1):
+            with pytest.raises(ValueError, match=name):
+                P.window_attention_backward_workspace(**(good | {name: x}))
+
+
 # ------------------------------------------------------------------ the sources
 
 def test_kernels_that_start_early_read_no_results_as_constants():
