@@ -83,7 +83,7 @@ struct AttendTcParams {
   int G;            // query heads per key head
   int pairs;        // pairs of row tiles of a key head
   int part_pairs;   // of one part of its heads
-  int splits;       // runs that a piece's tile list is cut into
+  int splits;       // runs that a piece's tile list is cut into (plain keys: 1)
   int items;        // pairs * B * Hkv * splits
   long long patience;  // cycles that all of a CTA's items may take
   Window win;
@@ -515,7 +515,7 @@ __device__ __noinline__ void mend_rows(const AttendTcParams& p, const AttendItem
     if (!real) continue;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      if (p.splits > 1) {
+      if (KV != kKvPlain && p.splits > 1) {
         float* f = p.part + to * D + c + k;
         if (odd(*f)) *f = x[k];
       } else {
@@ -958,7 +958,7 @@ __device__ __forceinline__ void attend_pass(const CUtensorMap& tmQ, const CUtens
       if (!ok) break;
       tc_fence_after();
       const float inv = l != 0.f ? 1.f / l : 0.f;  // l is NaN if a score was
-      const bool split_out = p.splits > 1;
+      const bool split_out = KV != kKvPlain && p.splits > 1;
       const size_t to = size_t(w.split) * size_t(p.B) * p.Hq * p.N + row;
       if constexpr (AGAIN) {
         if (done) mend_rows<D, KV>(p, w, mine, real, z, a, split_out ? to : row, o_addr, inv * exponent(127 + c));
@@ -1089,17 +1089,15 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 constexpr int kJoinThreads = 256;
 // Its blocks may start while the partial sums are still written: no loads through the read-only path.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendTcParams p, int paged) {
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendTcParams p) {
   constexpr int LANES = D / 4, ROWS = kJoinThreads / LANES;
   const int64_t rows = int64_t(p.B) * p.Hq * p.N, row = int64_t(blockIdx.x) * ROWS + threadIdx.x / LANES;
   const int c = threadIdx.x % LANES * 4;
   // every block waits, so that this grid does not end before the one it depends on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows) return;
-  if (paged) {
-    const int b = int(row / (int64_t(p.Hq) * p.N)), t = int(row % p.N);
-    if (t >= q_len_of(p.pages, b, p.N)) return;
-  }
+  const int b = int(row / (int64_t(p.Hq) * p.N)), t = int(row % p.N);
+  if (t >= q_len_of(p.pages, b, p.N)) return;
   float m = -INFINITY;
 #pragma unroll 4
   for (int s = 0; s < p.splits; ++s) m = fmaxf(m, __ldcg(p.part_lse + s * rows + row));

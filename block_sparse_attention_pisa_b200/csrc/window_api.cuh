@@ -196,7 +196,8 @@ pisa_status_t launch_attend_tc(pisa::AttendTcParams p, const void* K, const void
     PISA_TRY(make_code_map(&mV, V, D, uint64_t(page), uint64_t(num_pages) * p.Hkv, uint32_t(page)));
   }
   const int64_t rows = int64_t(p.B) * p.Hq * p.N;
-  if (p.splits > 1) {
+  const bool runs = KV != pisa::kKvPlain && p.splits > 1;
+  if (runs) {
     p.part = static_cast<float*>(workspace);
     p.part_lse = p.part + size_t(p.splits) * rows * D;
   }
@@ -204,10 +205,11 @@ pisa_status_t launch_attend_tc(pisa::AttendTcParams p, const void* K, const void
   PISA_TRY(set_smem(k, C::SMEM));
   k<<<unsigned(ctas), C::kThreads, C::SMEM, st>>>(mQ, mK, mV, p);
   PISA_TRY(check_launch("attend_tc_kernel"));
-  if (p.splits > 1) {
+  if constexpr (KV != pisa::kKvPlain) {
     constexpr int per = pisa::kJoinThreads / (D / 4);  // rows of a block
-    PISA_TRY(launch_behind(pisa::attend_join_kernel<D>, unsigned((rows + per - 1) / per), pisa::kJoinThreads, 0, st,
-                           "attend_join_kernel", p, int(KV != pisa::kKvPlain)));
+    if (runs)
+      PISA_TRY(launch_behind(pisa::attend_join_kernel<D>, unsigned((rows + per - 1) / per), pisa::kJoinThreads, 0, st,
+                             "attend_join_kernel", p));
   }
   return ok();
 }
@@ -338,7 +340,7 @@ pisa_status_t pisa_window_attention(const void* Q, const void* K, const void* V,
   a.Hkv = shape.Hkv;
   a.N = shape.N;
   a.scale = scale;
-  plan_attend(&a, 0);
+  plan_attend(&a, 0);  // no runs: the call has no workspace for their sums, and few heads leave SMs idle
   auto st = static_cast<cudaStream_t>(stream);
   return shape.d == 128 ? launch_attend_tc<128, pisa::kKvPlain>(a, K, V, 0, 0, nullptr, st)
                         : launch_attend_tc<64, pisa::kKvPlain>(a, K, V, 0, 0, nullptr, st);
