@@ -413,3 +413,52 @@ def test_keys_without_query_heads_have_no_gradient():
     out = torch.empty_like(Q), torch.full_like(K, 3.0), torch.full_like(K, 3.0)
     for grads in (P.window_attention_backward(Q, Q, K, K, O, lse), P.window_attention_backward(Q, Q, K, K, O, lse, out=out)):
         assert grads[0].shape == Q.shape and all(g.shape == K.shape and (g == 0).all() for g in grads[1:])
+
+
+def gradient64(do, q, k, v, see, scale):
+    """(dq, dk, dv, tol_dq, tol_dk, tol_dv) of one head in 64 bits on the device: the formulas and the
+    bounds of window_bounds.backward."""
+    u, f, d = T.U, 2.0 ** -24, q.shape[1]
+    n, top = k.shape[0], scale * float((q.abs() @ k.abs().mT).max())
+    e = 2 * (d + 8) * f * top + 2.0 ** -19
+    p = torch.softmax((scale * q @ k.mT).masked_fill_(~see, float("-inf")), 1)
+    o, dp = p @ v, do @ v.mT
+    delta = (p * dp).sum(1, keepdim=True)
+    tol_o = T.SLACK * ((u + e + n * f) * (p @ v.abs()) + u * o.abs())
+    t_delta = (do.abs() * tol_o).sum(1, keepdim=True)
+    ds = p * (dp - delta)
+    t_ds = p * (t_delta + e * (dp.abs() + delta.abs()) + d * f * (do.abs() @ v.abs().mT)) + (u + n * f) * ds.abs()
+    dq = scale * ds @ k
+    return (dq, scale * ds.mT @ q, p.mT @ do, T.SLACK * (scale * t_ds @ k.abs() + u * dq.abs()),
+            T.SLACK * scale * t_ds.mT @ q.abs(), T.SLACK * ((u + e + n * f) * p).mT @ do.abs())
+
+
+@pytest.mark.parametrize("shape", [
+    (1, 4, 1, 6000, 64, -1, 0, 0),       # 44 of 47 key tiles cut, 315 runs on 148 SMs
+    (2, 8, 2, 5003, 64, -1, 0, 0),       # 29 of 40, 376 runs
+    (1, 6, 2, 8200, 128, 700, 0, 300),   # 61 of 65, 338 runs
+    (1, 4, 2, 4100, 128, -1, -1, 0),     # all 33, 330 runs
+    (1, 16, 4, 9000, 128, 2047, 0, 64),  # one of 71: the first tokens'
+], ids=str)
+def test_gradient_in_several_waves(shape):
+    """Gradients whose runs of query tiles take more than one wave of the SMs, with many cut key tiles."""
+    B, Hq, Hkv, N, d, left, right, sinks = shape
+    Q, K, V, dO = make(B, Hq, Hkv, N, d, seed=56)
+    mask = dict(left=left, right=right, sinks=sinks)
+    O, lse = P.window_attention(Q, K, V, **mask)
+    grads = P.window_attention_backward(dO, Q, K, V, O, lse, **mask)
+    P.device_error()
+    see = torch.from_numpy(W.visible(np.arange(N), N, left, right, sinks)).cuda()
+    G = Hq // Hkv
+    for b in range(B):
+        for hk in range(Hkv):
+            sums = [0.0] * 4
+            for h in range(hk * G, (hk + 1) * G):
+                dq, dk, dv, tq, tk, tv = gradient64(dO[b, h].double(), Q[b, h].double(), K[b, hk].double(), V[b, hk].double(), see, d ** -0.5)
+                assert bool(((grads[0][b, h].double() - dq).abs() <= tq + T.LOST).all()), f"dQ[{b},{h}]"
+                assert float((grads[0][b, h].double() - dq).norm() / dq.norm()) <= T.U
+                sums = [x + y for x, y in zip(sums, (dk, dv, tk, tv))]
+            for got, want, tol, name in ((grads[1], sums[0], sums[2], "dK"), (grads[2], sums[1], sums[3], "dV")):
+                off = (got[b, hk].double() - want).abs()
+                assert bool((off <= tol + T.SLACK * T.U * want.abs() + T.LOST).all()), f"{name}[{b},{hk}]"
+                assert float(off.norm() / want.norm()) <= T.U
