@@ -720,7 +720,7 @@ def paged_attention(Q, cache, page_table, kv_lens, q_lens=None, left: int = -1, 
     """Attention of the new tokens Q (bf16 [B, Hq, N, d]; N = 1 for single tokens) over their
     sequences in the cache, which holds the new tokens too. Positions, ``kv_lens`` and
     ``q_lens`` as in ``cache_write``, the window as in ``window_attention`` (causal by
-    default). Returns (O bf16 [B, Hq, N, d], lse fp32 [B, Hq, N]); rows ``t >= q_lens[b]`` are
+    default). No gradient is recorded. Returns (O bf16 [B, Hq, N, d], lse fp32 [B, Hq, N]); rows ``t >= q_lens[b]`` are
     left as they are in ``out`` and ``lse``, zero without them. ``workspace``: a uint8 tensor
     of at least ``paged_attention_workspace`` bytes that no other call uses meanwhile."""
     import torch

@@ -28,8 +28,9 @@
 // Measured on 16384 tokens, 16 query and 4 key heads of 128, causal over 2048 keys: dQ 366 us (1.09
 // PFLOP/s of its 6 d flops per pair and query head; 500 us with strided loads of the rows and one
 // ring for K and V), dK and dV 547 us (0.97 of its 8 d), the join 11 us. What they wait for is each
-// other: the hand-offs between products and weights, which a third buffer would hide and tensor
-// memory has no room for. Cutting the runs by a model of their cost instead of evenly: 2% slower.
+// other: the hand-offs between products and weights. A third buffer would hide them; at D = 128 tensor
+// memory has no room for one (at D = 64, where dV, dK and two buffers take 384 columns, it has: not
+// built). Cutting the runs by a model of their cost instead of evenly: 2% slower.
 // The dK, dV kernel and the join set up while the kernel before them ends: a step on 2049 tokens,
 // 12 and 4 heads of 64, takes 67 us with that and 71 without.
 #pragma once

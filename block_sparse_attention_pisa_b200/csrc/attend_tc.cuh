@@ -43,15 +43,20 @@
 // 2 x 512 x 2 = 2048, as long as its 2 x 16384 exponentials take at 16 per cycle. Measured, a pair
 // takes about 4000: the softmax of two rows per scheduler 2300 (exponential 8 cycles per warp and
 // instruction, the pack to bf16 as long again, two fma and add per value), and then, of either group,
-// the chain "second half of P V, next Q K^T, its commit" that the other group only partly covers.
-// 2 x 24 heads of 4096 x 128, 512 keys to either side: 148 us, 0.65 PFLOP/s; 2 x 1024 tokens of 24
-// heads over a paged cache of 16 K, window 8192: 257 us, 0.81 PFLOP/s; D = 64 has the same softmax for
-// half the products. What was tried and measured slower: one 128-row tile with two score buffers;
+// the chain "second half of P V, next Q K^T, its commit" that the other group only partly covers. Products
+// and softmax of two groups could run beside each other in 2300; how the rest divides between that chain and
+// the registers that spill (a whole row of S in flight: 156-180 bytes, 460 in 8 bits) is not measured.
+// 2 x 24 heads of 4096 x 128, 512 keys to either side: 148-153 us by box, 0.64 PFLOP/s; 2 x 1024 tokens of
+// 24 heads over a paged cache of 16 K, window 8192: 274 us, 0.76 PFLOP/s; causal, 16 and 4 heads of 32 K x
+// 128: 4.1 ms, 1.07 PFLOP/s; D = 64 has the same softmax for half the products, and leaves 128 columns
+// of tensor memory unused. What was tried and measured slower: one 128-row tile with two score buffers;
 // two threads per row; a maximum guessed from the tile before; separate columns for P; packed fp32
 // pairs for the scaling; setmaxnreg (the roles that give registers away spill); the last wave's pairs
-// cut in two (one tile takes as long as a pair: its own chain).
-// 8 bits, D = 64: 3 sequences of 333 tokens, 12 and 4 heads, 5 K keys: 67 us; without the scales (128
-// products and 32 shared-memory loads of either kind per row and tile) 56, without the conversion 65.
+// cut in two (one tile takes as long as a pair: its own chain; 151 us against 147).
+// 8 bits, D = 64: 3 sequences of 333 tokens, 12 and 4 heads, 5 K keys: 62 us, all but about 10 (start and
+// join) for the 14 tiles of an item in turn: 7000 cycles a pair, where the bf16 form takes 4000. At 67 us
+// in all, it took 56 without the scales (128 products and 32 shared-memory loads of either kind per row
+// and tile) and 65 without the conversion; the rest is not accounted for.
 #pragma once
 
 #include "attention_tc.cuh"

@@ -24,7 +24,8 @@
 //
 // In 8 bits the products run in fp16, which holds every code exactly and which a conversion
 // instruction makes of two codes at once (putting codes into bf16 took more than half of the
-// instructions; products of 8-bit operands take 50 cycles each on this part's mma.sync). A power
+// instructions; a product of changing 8-bit operands takes 53 cycles on this part's mma.sync, the two
+// of 16 bits that replace it 16). A power
 // of two per row brings Q's largest value to [2^14, 2^15), so that values down to 2^-28 of it keep
 // bf16's 8 bits. The weights (softmax weight times the value's scale) have a factor of their own
 // per row that keeps the largest at 2^6 or more and below 2^15, apart from the maximum that the

@@ -280,7 +280,7 @@ pisa_status_t pisa_run_host_static(const void* Q, const void* K, const void* V, 
  * Sums and softmax statistics are fp32; the weights exp(s_j - m) (m a running maximum) and
  * the gradient's p_j and ds_j are rounded to bf16 for the tensor cores. A key or value that
  * a row does not see does not reach its O and lse, a NaN or an infinity either, and O is
- * finite wherever its values and scores are, of whatever size. The gradient
+ * finite wherever its values (up to 2^127) and scores are. The gradient
  * asks for finite operands: one that is not may reach every gradient of its key head. Every
  * sum runs in an order fixed by the shapes (and, over a cache, by the lengths): the same
  * call gives the same bits. A sum of n keys is off by up to n 2^-24 of sum p|v|, as fp32 sums
